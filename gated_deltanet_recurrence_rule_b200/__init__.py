@@ -11,16 +11,19 @@ from .api import (  # noqa: F401
     GDNError,
     decode_step,
     decode_tokens,
+    decode_tree,
     get_device_status,
     lib_path,
+    linear_decode_tokens,
     prefill,
     prefill_backward,
     prefill_backward_workspace_size,
     prefill_launch_count,
     prefill_uses_tensor_cores,
     prefill_workspace_size,
+    tree_commit,
 )
 
 __all__ = ["prefill", "prefill_backward", "decode_step", "decode_tokens", "prefill_workspace_size",
            "prefill_backward_workspace_size", "prefill_launch_count", "prefill_uses_tensor_cores",
-           "get_device_status", "GDNError", "GDN_INPUT_PREPARED", "GDN_INPUT_RAW", "lib_path"]
+           "get_device_status", "linear_decode_tokens", "decode_tree", "tree_commit", "GDNError", "GDN_INPUT_PREPARED", "GDN_INPUT_RAW", "lib_path"]

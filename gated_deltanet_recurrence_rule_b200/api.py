@@ -82,6 +82,13 @@ def load():
         for name in ("gdn_prefill_backward", "gdn_prefill_backward_sequential"):
             getattr(lib, name).restype = i32
             getattr(lib, name).argtypes = bwd_args
+        lib.gdn_linear_decode_tokens.restype = i32
+        lib.gdn_linear_decode_tokens.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, vp] + [i32] * 9 + [
+            f32, vp, vp]
+        lib.gdn_decode_tree.restype = i32
+        lib.gdn_decode_tree.argtypes = [vp] * 8 + [i32, vp] + [i32] * 10 + [f32, vp, vp]
+        lib.gdn_tree_commit.restype = i32
+        lib.gdn_tree_commit.argtypes = [vp] * 10 + [i32] * 10 + [vp, vp]
         lib.gdn_prefill_uses_tensor_cores.restype = i32
         lib.gdn_prefill_uses_tensor_cores.argtypes = [i32, i32, i32, i32, i32]
         lib.gdn_get_device_status.restype = i32
@@ -352,6 +359,141 @@ def prefill_backward_workspace_size(N, T, Hqk, Hv, Dk, Dv, sequential=False) -> 
     fn = (lib.gdn_prefill_backward_workspace_size_sequential if sequential
           else lib.gdn_prefill_backward_workspace_size)
     return int(fn(N, T, Hqk, Hv, Dk, Dv))
+
+
+def _check_tokens(q, k, v, what):
+    """Checks shared by the per-token entry points; q may be None.  Returns
+    (device, B, Tn, Hqk, Hv, Dk, Dv)."""
+    if not isinstance(k, torch.Tensor) or not k.is_cuda:
+        raise ValueError(f"{what} runs on a CUDA device only")
+    if k.dim() != 4 or not isinstance(v, torch.Tensor) or v.dim() != 4:
+        raise ValueError(f"{what}: k must be [B, tokens, Hqk, Dk] and v [B, tokens, Hv, Dv]")
+    B, Tn, Hqk, Dk = k.shape
+    Hv, Dv = v.shape[2], v.shape[3]
+    if k.dtype not in _DTYPE_CODE:
+        raise ValueError(f"unsupported dtype {k.dtype}")
+    if q is not None:
+        _require(q, "q", k.device, k.dtype, (B, Tn, Hqk, Dk))
+    _require(k, "k", k.device, k.dtype)
+    _require(v, "v", k.device, k.dtype, (B, Tn, Hv, Dv))
+    return k.device, B, Tn, Hqk, Hv, Dk, Dv
+
+
+def _check_pool(state_in, state_out, dev, Hv, Dv, Dk):
+    """Checks of the state pools; returns (num_slots, state dtype)."""
+    if not isinstance(state_in, torch.Tensor) or state_in.dtype not in _DTYPE_CODE:
+        raise ValueError("the state pool must be a bf16 or fp32 tensor")
+    shape = (state_in.shape[0] if state_in.dim() else 0, Hv, Dv, Dk)
+    _require(state_in, "state_in", dev, state_in.dtype, shape)
+    if state_out is not None:
+        _require(state_out, "state_out", dev, state_in.dtype, shape)
+    return shape[0], state_in.dtype
+
+
+def _check_ints(dev, **tensors):
+    for name, (t, shape) in tensors.items():
+        if t is not None:
+            _require(t, name, dev, torch.int32, shape)
+
+
+def _output(o, o_dtype, shape, dev):
+    if o is None:
+        if o_dtype not in _DTYPE_CODE:
+            raise ValueError(f"unsupported o dtype {o_dtype}")
+        return torch.empty(shape, dtype=o_dtype, device=dev)
+    if not isinstance(o, torch.Tensor) or o.dtype not in _DTYPE_CODE:
+        raise ValueError("o must be a bf16 or fp32 tensor")
+    _require(o, "o", dev, None, shape)
+    return o
+
+
+def linear_decode_tokens(q, k, v, g, state_in, state_out=None, src_slot=None, dst_slot=None, o=None,
+                         scale=1.0, o_dtype=torch.float32, device_status=None):
+    """Linear attention with a decay for each head, 1 to 16 new tokens of each
+    sequence against a pool of states: S_t = e^g S_{t-1} + v_t k_t^T,
+    o_t = scale S_t q_t.
+
+    g [Hv] fp32 (log of the head's decay, <= 0); everything else as in
+    ``decode_tokens``.  Returns o [B, Tn, Hv, Dv]."""
+    lib = load()
+    dev, B, Tn, Hqk, Hv, Dk, Dv = _check_tokens(q, k, v, "linear_decode_tokens")
+    _require(g, "g", dev, torch.float32, (Hv,))
+    if state_out is None:
+        state_out = state_in
+    num_slots, sdt = _check_pool(state_in, state_out, dev, Hv, Dv, Dk)
+    _check_ints(dev, src_slot=(src_slot, (B,)), dst_slot=(dst_slot, (B,)), device_status=(device_status, (1,)))
+    o = _output(o, o_dtype, (B, Tn, Hv, Dv), dev)
+    with torch.cuda.device(dev):
+        st = lib.gdn_linear_decode_tokens(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state_in),
+                                          _ptr(state_out), _ptr(src_slot), _ptr(dst_slot), num_slots,
+                                          _ptr(o), B, Tn, Hqk, Hv, Dk, Dv, _DTYPE_CODE[k.dtype],
+                                          _DTYPE_CODE[o.dtype], _DTYPE_CODE[sdt], float(scale),
+                                          _ptr(device_status), _stream(dev))
+    _check(st, "gdn_linear_decode_tokens")
+    return o
+
+
+def _check_gates(g, beta, raw_inputs, dev, B, M, Hv):
+    if beta is None:
+        if raw_inputs:
+            raise ValueError("raw_inputs needs the delta rule's gates (beta is None)")
+        _require(g, "g", dev, torch.float32, (Hv,))
+    else:
+        _require(g, "g", dev, torch.float32, (B, M, Hv))
+        _require(beta, "beta", dev, torch.float32, (B, M, Hv))
+
+
+def decode_tree(q, k, v, g, beta, parent, state, src_slot=None, o=None, scale=1.0,
+                o_dtype=torch.float32, device_status=None, raw_inputs=False):
+    """Outputs of every node of a tree of drafted tokens over the cached states,
+    which are left as they are.
+
+    q, k [B, M, Hqk, Dk]; v [B, M, Hv, Dv]; M <= 64 nodes; parent [B, M] int32:
+    an earlier node, -1 for the cached state, below -1 for a padding node (its o
+    row is left untouched).  Gated delta rule: g, beta [B, M, Hv] fp32; with
+    ``beta`` None the linear rule of ``linear_decode_tokens``, g [Hv].
+    state [num_slots, Hv, Dv, Dk] fp32 or bf16; src_slot [B] int32 or None
+    (slot b), negative for a padding sequence.  Returns o [B, M, Hv, Dv]."""
+    lib = load()
+    dev, B, M, Hqk, Hv, Dk, Dv = _check_tokens(q, k, v, "decode_tree")
+    _check_gates(g, beta, raw_inputs, dev, B, M, Hv)
+    _require(parent, "parent", dev, torch.int32, (B, M))
+    num_slots, sdt = _check_pool(state, None, dev, Hv, Dv, Dk)
+    _check_ints(dev, src_slot=(src_slot, (B,)), device_status=(device_status, (1,)))
+    o = _output(o, o_dtype, (B, M, Hv, Dv), dev)
+    with torch.cuda.device(dev):
+        st = lib.gdn_decode_tree(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(parent), _ptr(state),
+                                 _ptr(src_slot), num_slots, _ptr(o), B, M, Hqk, Hv, Dk, Dv,
+                                 _DTYPE_CODE[k.dtype], _DTYPE_CODE[o.dtype], _DTYPE_CODE[sdt],
+                                 GDN_INPUT_RAW if raw_inputs else GDN_INPUT_PREPARED, float(scale),
+                                 _ptr(device_status), _stream(dev))
+    _check(st, "gdn_decode_tree")
+    return o
+
+
+def tree_commit(k, v, g, beta, parent, accept, state_in, state_out=None, src_slot=None, dst_slot=None,
+                device_status=None, raw_inputs=False):
+    """Write the state after node ``accept[b]`` of each tree to its slot (the
+    cached state itself where accept[b] is -1), from the same k, v, g, beta and
+    parent as ``decode_tree`` was given.  accept [B] int32; pools and slots as in
+    ``decode_tokens``.  Returns state_out."""
+    lib = load()
+    dev, B, M, Hqk, Hv, Dk, Dv = _check_tokens(None, k, v, "tree_commit")
+    _check_gates(g, beta, raw_inputs, dev, B, M, Hv)
+    _require(parent, "parent", dev, torch.int32, (B, M))
+    _require(accept, "accept", dev, torch.int32, (B,))
+    if state_out is None:
+        state_out = state_in
+    num_slots, sdt = _check_pool(state_in, state_out, dev, Hv, Dv, Dk)
+    _check_ints(dev, src_slot=(src_slot, (B,)), dst_slot=(dst_slot, (B,)), device_status=(device_status, (1,)))
+    with torch.cuda.device(dev):
+        st = lib.gdn_tree_commit(_ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(parent), _ptr(accept),
+                                 _ptr(state_in), _ptr(state_out), _ptr(src_slot), _ptr(dst_slot), num_slots,
+                                 B, M, Hqk, Hv, Dk, Dv, _DTYPE_CODE[k.dtype], _DTYPE_CODE[sdt],
+                                 GDN_INPUT_RAW if raw_inputs else GDN_INPUT_PREPARED, _ptr(device_status),
+                                 _stream(dev))
+    _check(st, "gdn_tree_commit")
+    return state_out
 
 
 def prefill_uses_tensor_cores(Hqk, Hv, Dk, Dv, dtype=torch.bfloat16) -> bool:

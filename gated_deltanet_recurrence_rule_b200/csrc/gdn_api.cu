@@ -56,6 +56,23 @@ cudaError_t launch_backward(const void *q, const void *k, const void *v, const f
                             const float *dO, const float *dSfin, float *dq, float *dk, float *dv,
                             float *dg, float *dbeta, float *ds0, void *workspace,
                             cudaStream_t stream);
+int linear_decode_tokens_max();
+cudaError_t launch_linear_decode(const void *q, const void *k, const void *v, const float *g,
+                                 const void *state_in, void *state_out, const int32_t *src_slot,
+                                 const int32_t *dst_slot, int num_slots, void *o, int B, int Tn,
+                                 int Hqk, int Hv, int Dk, int Dv, int dtype, int o_dtype,
+                                 int state_dtype, float scale, int32_t *status, cudaStream_t stream);
+int tree_max_nodes();
+cudaError_t launch_decode_tree(const void *q, const void *k, const void *v, const float *g,
+                               const float *beta, const int32_t *parent, const void *state,
+                               const int32_t *src_slot, int num_slots, void *o, int B, int M, int Hqk,
+                               int Hv, int Dk, int Dv, int dtype, int o_dtype, int state_dtype,
+                               int input_form, float scale, int32_t *status, cudaStream_t stream);
+cudaError_t launch_tree_commit(const void *k, const void *v, const float *g, const float *beta,
+                               const int32_t *parent, const int32_t *accept, const void *state_in,
+                               void *state_out, const int32_t *src_slot, const int32_t *dst_slot,
+                               int num_slots, int B, int M, int Hqk, int Hv, int Dk, int Dv, int dtype,
+                               int state_dtype, int input_form, int32_t *status, cudaStream_t stream);
 }  // namespace gdn
 
 namespace {
@@ -352,6 +369,100 @@ int32_t gdn_prefill_backward_sequential(const void *q, const void *k, const void
       q, k, v, g, beta, cu_seqlens, num_seqs, total_tokens, num_qk_heads, num_v_heads, head_dim_k,
       head_dim_v, dtype, scale, initial_state, d_o, d_final_state, dq, dk, dv, dg, dbeta,
       d_initial_state, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t gdn_linear_decode_tokens(const void *q, const void *k, const void *v, const float *g,
+                                 const void *state_in, void *state_out, const int32_t *src_slot,
+                                 const int32_t *dst_slot, int32_t num_slots, void *o, int32_t batch,
+                                 int32_t tokens, int32_t num_qk_heads, int32_t num_v_heads,
+                                 int32_t head_dim_k, int32_t head_dim_v, int32_t dtype,
+                                 int32_t o_dtype, int32_t state_dtype, float scale,
+                                 int32_t *device_status, void *stream) {
+  if (batch < 0 || tokens < 0 || num_slots < 0) return GDN_ERR_INVALID_ARG;
+  if (!dims_ok(num_qk_heads, num_v_heads, head_dim_k, head_dim_v, dtype)) return GDN_ERR_INVALID_ARG;
+  if (!dtype_ok(o_dtype) || !dtype_ok(state_dtype)) return GDN_ERR_INVALID_ARG;
+  if (!dims_supported(head_dim_k, head_dim_v)) return GDN_ERR_UNSUPPORTED;
+  if (tokens > gdn::linear_decode_tokens_max()) return GDN_ERR_UNSUPPORTED;
+  if (batch == 0 || tokens == 0) return GDN_OK;
+  if ((int64_t)batch * num_v_heads > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  if (!q || !k || !v || !g || !state_in || !state_out || !o) return GDN_ERR_INVALID_ARG;
+  if (!src_slot && batch > num_slots) return GDN_ERR_INVALID_ARG;  // slot b for sequence b
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) ||
+      !aligned(state_in, 16) || !aligned(state_out, 16) || !aligned(g, 4) ||
+      (src_slot && !aligned(src_slot, 4)) || (dst_slot && !aligned(dst_slot, 4)) ||
+      (device_status && !aligned(device_status, 4)))
+    return GDN_ERR_INVALID_ARG;
+  return cuda_status(gdn::launch_linear_decode(
+      q, k, v, g, state_in, state_out, src_slot, dst_slot, num_slots, o, batch, tokens, num_qk_heads,
+      num_v_heads, head_dim_k, head_dim_v, dtype, o_dtype, state_dtype, scale, device_status,
+      static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+// Host checks shared by the two tree entry points: GDN_OK to proceed,
+// kNothingToDo, or an error code.
+int32_t check_tree(const void *k, const void *v, const float *g, const float *beta,
+                   const int32_t *parent, const void *state, const int32_t *src_slot,
+                   int32_t num_slots, int32_t batch, int32_t nodes, int32_t num_qk_heads,
+                   int32_t num_v_heads, int32_t head_dim_k, int32_t head_dim_v, int32_t dtype,
+                   int32_t state_dtype, int32_t input_form, const int32_t *device_status) {
+  if (batch < 0 || nodes < 0 || num_slots < 0) return GDN_ERR_INVALID_ARG;
+  if (!form_ok(input_form) || !dtype_ok(state_dtype)) return GDN_ERR_INVALID_ARG;
+  if (!dims_ok(num_qk_heads, num_v_heads, head_dim_k, head_dim_v, dtype)) return GDN_ERR_INVALID_ARG;
+  if (!dims_supported(head_dim_k, head_dim_v)) return GDN_ERR_UNSUPPORTED;
+  if (nodes > gdn::tree_max_nodes()) return GDN_ERR_UNSUPPORTED;
+  if (batch == 0 || nodes == 0) return kNothingToDo;
+  if ((int64_t)batch * num_v_heads > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  if (!k || !v || !g || !parent || !state) return GDN_ERR_INVALID_ARG;
+  if (!beta && input_form == GDN_INPUT_RAW) return GDN_ERR_INVALID_ARG;  // no gates to map
+  if (!src_slot && batch > num_slots) return GDN_ERR_INVALID_ARG;        // slot b for sequence b
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(state, 16) || !aligned(g, 4) ||
+      (beta && !aligned(beta, 4)) || !aligned(parent, 4) || (src_slot && !aligned(src_slot, 4)) ||
+      (device_status && !aligned(device_status, 4)))
+    return GDN_ERR_INVALID_ARG;
+  return GDN_OK;
+}
+
+}  // namespace
+
+int32_t gdn_decode_tree(const void *q, const void *k, const void *v, const float *g,
+                        const float *beta, const int32_t *parent, const void *state,
+                        const int32_t *src_slot, int32_t num_slots, void *o, int32_t batch,
+                        int32_t nodes, int32_t num_qk_heads, int32_t num_v_heads,
+                        int32_t head_dim_k, int32_t head_dim_v, int32_t dtype, int32_t o_dtype,
+                        int32_t state_dtype, int32_t input_form, float scale,
+                        int32_t *device_status, void *stream) {
+  if (!dtype_ok(o_dtype)) return GDN_ERR_INVALID_ARG;
+  const int32_t c = check_tree(k, v, g, beta, parent, state, src_slot, num_slots, batch, nodes,
+                               num_qk_heads, num_v_heads, head_dim_k, head_dim_v, dtype, state_dtype,
+                               input_form, device_status);
+  if (c != GDN_OK) return c == kNothingToDo ? GDN_OK : c;
+  if (!q || !o || !aligned(q, 16) || !aligned(o, 16)) return GDN_ERR_INVALID_ARG;
+  return cuda_status(gdn::launch_decode_tree(
+      q, k, v, g, beta, parent, state, src_slot, num_slots, o, batch, nodes, num_qk_heads, num_v_heads,
+      head_dim_k, head_dim_v, dtype, o_dtype, state_dtype, input_form, scale, device_status,
+      static_cast<cudaStream_t>(stream)));
+}
+
+int32_t gdn_tree_commit(const void *k, const void *v, const float *g, const float *beta,
+                        const int32_t *parent, const int32_t *accept, const void *state_in,
+                        void *state_out, const int32_t *src_slot, const int32_t *dst_slot,
+                        int32_t num_slots, int32_t batch, int32_t nodes, int32_t num_qk_heads,
+                        int32_t num_v_heads, int32_t head_dim_k, int32_t head_dim_v, int32_t dtype,
+                        int32_t state_dtype, int32_t input_form, int32_t *device_status,
+                        void *stream) {
+  const int32_t c = check_tree(k, v, g, beta, parent, state_in, src_slot, num_slots, batch, nodes,
+                               num_qk_heads, num_v_heads, head_dim_k, head_dim_v, dtype, state_dtype,
+                               input_form, device_status);
+  if (c != GDN_OK) return c == kNothingToDo ? GDN_OK : c;
+  if (!accept || !state_out || !aligned(accept, 4) || !aligned(state_out, 16) ||
+      (dst_slot && !aligned(dst_slot, 4)))
+    return GDN_ERR_INVALID_ARG;
+  return cuda_status(gdn::launch_tree_commit(
+      k, v, g, beta, parent, accept, state_in, state_out, src_slot, dst_slot, num_slots, batch, nodes,
+      num_qk_heads, num_v_heads, head_dim_k, head_dim_v, dtype, state_dtype, input_form, device_status,
+      static_cast<cudaStream_t>(stream)));
 }
 
 int32_t gdn_prefill_uses_tensor_cores(int32_t num_qk_heads, int32_t num_v_heads,

@@ -415,6 +415,93 @@ int32_t gdn_prefill_backward_sequential(const void *q, const void *k, const void
                                         void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Linear attention with a decay for each head: the same fixed-size state without
+ * the erase, S (Dv x Dk) of every (sequence, value head), lam_h = exp(g_h) a
+ * constant of the head,
+ *
+ *     S_t = lam_h S_{t-1} + v_t k_t^T,     o_t = scale * S_t q_t.
+ *
+ * Heads, packed sequences, state layout, slot pools and element types are those
+ * of the entry points above.  g is [Hv] fp32, <= 0; values below -30 (and -inf,
+ * lam = 0) are taken as -30: e^-30 is below the resolution of an fp32 sum.  (The
+ * pages describe the gated rule only; this is its relative without the erase.)
+ *
+ * gdn_linear_decode_tokens: `tokens` new tokens for each of `batch` sequences
+ * against a pool of states.  Arguments, slots, padding entries and errors as in
+ * gdn_decode_tokens, without beta and input_form, and with g [Hv].
+ * Supported: 1 <= tokens <= 16; Hv % Hqk == 0; Dk, Dv in {64, 128}.
+ */
+int32_t gdn_linear_decode_tokens(const void *q, const void *k, const void *v, const float *g,
+                                 const void *state_in, void *state_out, const int32_t *src_slot,
+                                 const int32_t *dst_slot, int32_t num_slots, void *o, int32_t batch,
+                                 int32_t tokens, int32_t num_qk_heads, int32_t num_v_heads,
+                                 int32_t head_dim_k, int32_t head_dim_v, int32_t dtype,
+                                 int32_t o_dtype, int32_t state_dtype, float scale,
+                                 int32_t *device_status, void *stream);
+
+/*
+ * Verification of a tree of drafted tokens over the cached states (speculative
+ * decoding with several continuations per position; gdn_decode_tokens takes one
+ * chain).  Node i of a sequence's tree continues its parent p = parent[i]: an
+ * earlier node (p < i), or the cached state (p = -1; a tree may have several such
+ * nodes).  Per node, with a_i = exp(g_i),
+ *
+ *     S_i = a_i S_p (I - beta_i k_i k_i^T) + beta_i v_i k_i^T,   o_i = scale * S_i q_i,
+ *
+ * or, where beta is NULL, the linear rule S_i = lam_h S_p + v_i k_i^T with
+ * g [Hv].  The states are read once and not written; gdn_tree_commit writes the
+ * accepted one.  A node sees its ancestors and the cached state only: nothing of
+ * another branch, infinities and NaN included, reaches it.
+ *
+ *   q, k        [batch, nodes, Hqk, Dk]   dtype
+ *   v           [batch, nodes, Hv, Dv]    dtype
+ *   g, beta     [batch, nodes, Hv]        fp32; or beta NULL and g [Hv]
+ *   parent      [batch, nodes] int32, device.  An entry below -1 marks a padding
+ *               node: its q, k, v are not read and its o is left untouched.
+ *   state       [num_slots, Hv, Dv, Dk]   state_dtype, pool read
+ *   src_slot    [batch] int32, device: slot of sequence b; NULL means slot b.  A
+ *               negative entry marks padding: its o is left untouched.
+ *   o           [batch, nodes, Hv, Dv]    o_dtype (output)
+ *   input_form  as for gdn_decode_tokens; GDN_INPUT_PREPARED where beta is NULL
+ *   device_status  optional device int32: a slot index >= num_slots, or a parent
+ *               that is no earlier node of its tree (itself, a later one, or a
+ *               padding node), is recorded as GDN_ERR_INVALID_ARG there and that
+ *               sequence is skipped.
+ *
+ * Arithmetic: products of S with k and q on tensor cores, fp32 accumulation; the
+ * state (and fp32 k, q) enter as three bf16 terms (24 bits), as two (16 bits)
+ * where inputs and o are bf16.  Supported: 1 <= nodes <= 64; Hv % Hqk == 0;
+ * Dk, Dv in {64, 128}.  batch = 0 or nodes = 0 is a valid no-op.
+ */
+int32_t gdn_decode_tree(const void *q, const void *k, const void *v, const float *g,
+                        const float *beta, const int32_t *parent, const void *state,
+                        const int32_t *src_slot, int32_t num_slots, void *o, int32_t batch,
+                        int32_t nodes, int32_t num_qk_heads, int32_t num_v_heads,
+                        int32_t head_dim_k, int32_t head_dim_v, int32_t dtype, int32_t o_dtype,
+                        int32_t state_dtype, int32_t input_form, float scale,
+                        int32_t *device_status, void *stream);
+
+/*
+ * The state after the accepted node of each tree, from the same k, v, g, beta and
+ * parent as gdn_decode_tree was given: state_out[dst_slot[b]] becomes the state
+ * after node accept[b], the cached state itself (a copy) where accept[b] = -1.
+ * fp32 arithmetic along the path; a bf16 state is rounded once.
+ *
+ *   accept      [batch] int32, device: a node of tree b, or -1
+ *   state_in, state_out, src_slot, dst_slot, num_slots   as for gdn_decode_tokens
+ *   device_status  optional: a bad slot, an accept outside [-1, nodes), or a path
+ *               that meets a bad parent or a padding node, is recorded as
+ *               GDN_ERR_INVALID_ARG there and nothing is written for that sequence.
+ */
+int32_t gdn_tree_commit(const void *k, const void *v, const float *g, const float *beta,
+                        const int32_t *parent, const int32_t *accept, const void *state_in,
+                        void *state_out, const int32_t *src_slot, const int32_t *dst_slot,
+                        int32_t num_slots, int32_t batch, int32_t nodes, int32_t num_qk_heads,
+                        int32_t num_v_heads, int32_t head_dim_k, int32_t head_dim_v, int32_t dtype,
+                        int32_t state_dtype, int32_t input_form, int32_t *device_status,
+                        void *stream);
+
+/*
  * 1 if gdn_prefill with these sizes and dtype runs the tensor-core (tcgen05)
  * kernel, 0 if it runs the fp32 CUDA-core kernel or the arguments are invalid.
  * Host only; touches no device.

@@ -1,0 +1,102 @@
+"""Host-side refusals of the linear-attention and token-tree entry points (no GPU
+needed, no kernel launched; the fake addresses are never dereferenced)."""
+import pytest
+import torch
+
+from gated_deltanet_recurrence_rule_b200 import api
+
+BAD, UNSUP, OK = api.GDN_ERR_INVALID_ARG, api.GDN_ERR_UNSUPPORTED, api.GDN_OK
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from gated_deltanet_recurrence_rule_b200 import build
+
+    build.build()
+    return api.load()
+
+
+P = 1 << 12
+DIMS = dict(Hqk=2, Hv=6, Dk=64, Dv=64)
+
+
+def decode(lib, **kw):
+    a = dict(q=P, k=P, v=P, g=P, si=P, so=P, src=None, dst=None, slots=4, o=P, B=2, Tn=3, dt=0, odt=1, sdt=1,
+             status=None, **DIMS)
+    a.update(kw)
+    return lib.gdn_linear_decode_tokens(a["q"], a["k"], a["v"], a["g"], a["si"], a["so"], a["src"], a["dst"],
+                                        a["slots"], a["o"], a["B"], a["Tn"], a["Hqk"], a["Hv"], a["Dk"], a["Dv"],
+                                        a["dt"], a["odt"], a["sdt"], 1.0, a["status"], None)
+
+
+def tree(lib, **kw):
+    a = dict(q=P, k=P, v=P, g=P, beta=P, par=P, s=P, src=None, slots=4, o=P, B=2, M=3, dt=0, odt=1, sdt=1, form=0,
+             status=None, **DIMS)
+    a.update(kw)
+    return lib.gdn_decode_tree(a["q"], a["k"], a["v"], a["g"], a["beta"], a["par"], a["s"], a["src"], a["slots"],
+                               a["o"], a["B"], a["M"], a["Hqk"], a["Hv"], a["Dk"], a["Dv"], a["dt"], a["odt"],
+                               a["sdt"], a["form"], 1.0, a["status"], None)
+
+
+def commit(lib, **kw):
+    a = dict(k=P, v=P, g=P, beta=P, par=P, acc=P, si=P, so=P, src=None, dst=None, slots=4, B=2, M=3, dt=0, sdt=1,
+             form=0, status=None, **DIMS)
+    a.update(kw)
+    return lib.gdn_tree_commit(a["k"], a["v"], a["g"], a["beta"], a["par"], a["acc"], a["si"], a["so"], a["src"],
+                               a["dst"], a["slots"], a["B"], a["M"], a["Hqk"], a["Hv"], a["Dk"], a["Dv"], a["dt"],
+                               a["sdt"], a["form"], a["status"], None)
+
+
+@pytest.mark.parametrize("call", [decode, tree, commit])
+def test_common_refusals(lib, call):
+    assert call(lib, Hv=5) == BAD and call(lib, Hqk=0) == BAD and call(lib, Hv=-6) == BAD
+    assert call(lib, dt=2) == BAD and call(lib, sdt=2) == BAD
+    assert call(lib, Dk=96) == UNSUP and call(lib, Dv=256) == UNSUP and call(lib, Dk=0) == BAD
+    assert call(lib, B=-1) == BAD and call(lib, slots=-1) == BAD
+    assert call(lib, B=5) == BAD                       # no slot map: needs batch <= slots
+    assert call(lib, B=2 ** 30, slots=2 ** 30) == UNSUP  # more CTAs than a grid takes
+    for name in ("k", "v", "g"):
+        assert call(lib, **{name: None}) == BAD
+        assert call(lib, **{name: P + 2}) == BAD       # misaligned
+    assert call(lib, src=P + 1) == BAD and call(lib, status=P + 2) == BAD
+    assert call(lib, B=0) == OK
+
+
+def test_decode_refusals(lib):
+    assert decode(lib, Tn=17) == UNSUP and decode(lib, Tn=-1) == BAD and decode(lib, Tn=0) == OK
+    assert decode(lib, odt=7) == BAD
+    for name in ("q", "si", "so", "o"):
+        assert decode(lib, **{name: None}) == BAD
+    for name in ("q", "si", "so", "o"):
+        assert decode(lib, **{name: P + 8}) == BAD
+
+
+def test_tree_refusals(lib):
+    assert tree(lib, M=65) == UNSUP and tree(lib, M=-1) == BAD and tree(lib, M=0) == OK
+    assert tree(lib, form=5) == BAD and tree(lib, odt=7) == BAD
+    assert tree(lib, beta=None, form=1) == BAD         # the linear rule has no gates to map
+    for name in ("q", "par", "s", "o"):
+        assert tree(lib, **{name: None}) == BAD
+    assert tree(lib, par=P + 2) == BAD and tree(lib, s=P + 8) == BAD and tree(lib, beta=P + 2) == BAD
+
+
+def test_commit_refusals(lib):
+    assert commit(lib, M=65) == UNSUP and commit(lib, M=0) == OK
+    assert commit(lib, form=5) == BAD and commit(lib, beta=None, form=1) == BAD
+    for name in ("par", "acc", "si", "so"):
+        assert commit(lib, **{name: None}) == BAD
+    assert commit(lib, acc=P + 2) == BAD and commit(lib, so=P + 8) == BAD and commit(lib, dst=P + 1) == BAD
+
+
+def test_python_refuses_cpu_tensors(lib):
+    x = torch.zeros(1, 2, 2, 64)
+    v = torch.zeros(1, 2, 6, 64)
+    s = torch.zeros(1, 6, 64, 64)
+    g = torch.zeros(6)
+    p = torch.zeros(1, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.linear_decode_tokens(x, x, v, g, s)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.decode_tree(x, x, v, g, None, p, s)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.tree_commit(x, v, g, None, p, p[:, 0], s)
