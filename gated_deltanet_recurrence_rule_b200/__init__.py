@@ -15,6 +15,9 @@ from .api import (  # noqa: F401
     get_device_status,
     lib_path,
     linear_decode_tokens,
+    linear_prefill,
+    linear_prefill_backward,
+    linear_prefill_workspace_size,
     prefill,
     prefill_backward,
     prefill_backward_workspace_size,
@@ -26,4 +29,6 @@ from .api import (  # noqa: F401
 
 __all__ = ["prefill", "prefill_backward", "decode_step", "decode_tokens", "prefill_workspace_size",
            "prefill_backward_workspace_size", "prefill_launch_count", "prefill_uses_tensor_cores",
-           "get_device_status", "linear_decode_tokens", "decode_tree", "tree_commit", "GDNError", "GDN_INPUT_PREPARED", "GDN_INPUT_RAW", "lib_path"]
+           "linear_prefill", "linear_prefill_backward", "linear_prefill_workspace_size",
+           "linear_decode_tokens", "decode_tree", "tree_commit", "get_device_status", "GDNError",
+           "GDN_INPUT_PREPARED", "GDN_INPUT_RAW", "lib_path"]

@@ -82,6 +82,12 @@ def load():
         for name in ("gdn_prefill_backward", "gdn_prefill_backward_sequential"):
             getattr(lib, name).restype = i32
             getattr(lib, name).argtypes = bwd_args
+        lib.gdn_linear_prefill_workspace_size.restype = sz
+        lib.gdn_linear_prefill_workspace_size.argtypes = [i32, i64] + [i32] * 6
+        lib.gdn_linear_prefill.restype = i32
+        lib.gdn_linear_prefill.argtypes = [vp] * 5 + [i32, i64] + [i32] * 7 + [f32, vp, vp, vp, vp, sz, vp]
+        lib.gdn_linear_prefill_backward.restype = i32
+        lib.gdn_linear_prefill_backward.argtypes = [vp] * 5 + [i32, i64] + [i32] * 5 + [f32] + [vp] * 8 + [sz, vp]
         lib.gdn_linear_decode_tokens.restype = i32
         lib.gdn_linear_decode_tokens.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, vp] + [i32] * 9 + [
             f32, vp, vp]
@@ -405,6 +411,108 @@ def _output(o, o_dtype, shape, dev):
         raise ValueError("o must be a bf16 or fp32 tensor")
     _require(o, "o", dev, None, shape)
     return o
+
+
+def linear_prefill_workspace_size(num_seqs, total_tokens, Hqk, Hv, Dk, Dv, dtype=torch.bfloat16,
+                                  backward=False) -> int:
+    """Workspace bytes for linear_prefill, or with ``backward`` for
+    linear_prefill_backward (0 for invalid sizes)."""
+    return int(load().gdn_linear_prefill_workspace_size(num_seqs, total_tokens, Hqk, Hv, Dk, Dv,
+                                                        _DTYPE_CODE[dtype], int(backward)))
+
+
+def _check_packed(q, k, v, g, cu_seqlens, what):
+    """Checks shared by linear prefill and its backward.  Returns (device, T, N,
+    Hqk, Hv, Dk, Dv, cu_seqlens)."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise ValueError(f"{what} runs on a CUDA device only")
+    if q.dim() != 3 or not isinstance(v, torch.Tensor) or v.dim() != 3:
+        raise ValueError(f"{what}: q must be [T, Hqk, Dk] and v [T, Hv, Dv]")
+    dev = q.device
+    T, Hqk, Dk = q.shape
+    Hv, Dv = v.shape[1], v.shape[2]
+    if q.dtype not in _DTYPE_CODE:
+        raise ValueError(f"unsupported dtype {q.dtype}")
+    _require(q, "q", dev, q.dtype)
+    _require(k, "k", dev, q.dtype, (T, Hqk, Dk))
+    _require(v, "v", dev, q.dtype, (T, Hv, Dv))
+    _require(g, "g", dev, torch.float32, (Hv,))
+    if cu_seqlens is None:
+        cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=dev)
+    _require(cu_seqlens, "cu_seqlens", dev, torch.int32)
+    if cu_seqlens.dim() != 1 or not cu_seqlens.numel():
+        raise ValueError("cu_seqlens must hold num_seqs + 1 offsets")
+    return dev, T, cu_seqlens.numel() - 1, Hqk, Hv, Dk, Dv, cu_seqlens
+
+
+def _workspace(workspace, need, dev):
+    if workspace is None:
+        workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=dev)
+    _require(workspace, "workspace", dev, torch.uint8)
+    return workspace
+
+
+def linear_prefill(q, k, v, g, cu_seqlens=None, initial_state=None, output_final_state=True,
+                   final_state=None, scale=1.0, o=None, workspace=None, o_dtype=torch.float32,
+                   state_dtype=None):
+    """Linear attention with a decay for each head over packed sequences:
+    S_t = e^g S_{t-1} + v_t k_t^T, o_t = scale S_t q_t, chunked.
+
+    g [Hv] fp32 (log of the head's decay, <= 0); everything else as in
+    ``prefill``.  ``workspace``: a zero-filled uint8 CUDA tensor of
+    ``linear_prefill_workspace_size`` bytes, reused across calls, or None.
+    bf16 inputs with ``o_dtype`` bf16 at head dim 128 run on the tensor cores.
+    Returns (o [T, Hv, Dv], final_state or None)."""
+    lib = load()
+    dev, T, N, Hqk, Hv, Dk, Dv, cu_seqlens = _check_packed(q, k, v, g, cu_seqlens, "linear_prefill")
+    sshape = (N, Hv, Dv, Dk)
+    given = [t.dtype for t in (initial_state, final_state) if t is not None]
+    sdt = given[0] if given else (state_dtype or torch.float32)
+    if sdt not in _DTYPE_CODE or (state_dtype is not None and state_dtype != sdt):
+        raise ValueError(f"unsupported or inconsistent state dtype {sdt}")
+    if initial_state is not None:
+        _require(initial_state, "initial_state", dev, sdt, sshape)
+    if final_state is None and output_final_state:
+        final_state = torch.empty(sshape, dtype=sdt, device=dev)
+    if final_state is not None:
+        _require(final_state, "final_state", dev, sdt, sshape)
+    o = _output(o, o_dtype, (T, Hv, Dv), dev)
+    with torch.cuda.device(dev):
+        need = linear_prefill_workspace_size(N, T, Hqk, Hv, Dk, Dv, q.dtype)
+        workspace = _workspace(workspace, need, dev)
+        st = lib.gdn_linear_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(cu_seqlens), N, T, Hqk, Hv, Dk,
+                                    Dv, _DTYPE_CODE[q.dtype], _DTYPE_CODE[o.dtype], _DTYPE_CODE[sdt],
+                                    float(scale), _ptr(initial_state), _ptr(final_state), _ptr(o),
+                                    _ptr(workspace), workspace.numel(), _stream(dev))
+    _check(st, "gdn_linear_prefill")
+    return o, final_state
+
+
+def linear_prefill_backward(q, k, v, g, d_o, cu_seqlens=None, initial_state=None, d_final_state=None,
+                            scale=1.0, workspace=None, want_d_initial_state=True):
+    """Gradients of linear_prefill given d_o [T, Hv, Dv] and optionally
+    d_final_state [N, Hv, Dv, Dk] fp32 (g is a constant of the layer).  d_o has
+    q's dtype, as the gradients do; states are fp32.  Returns (dq, dk, dv,
+    d_initial_state or None)."""
+    lib = load()
+    dev, T, N, Hqk, Hv, Dk, Dv, cu_seqlens = _check_packed(q, k, v, g, cu_seqlens, "linear_prefill_backward")
+    _require(d_o, "d_o", dev, q.dtype, (T, Hv, Dv))
+    sshape = (N, Hv, Dv, Dk)
+    for name, t in (("initial_state", initial_state), ("d_final_state", d_final_state)):
+        if t is not None:
+            _require(t, name, dev, torch.float32, sshape)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    ds0 = torch.empty(sshape, dtype=torch.float32, device=dev) if want_d_initial_state else None
+    with torch.cuda.device(dev):
+        need = linear_prefill_workspace_size(N, T, Hqk, Hv, Dk, Dv, q.dtype, backward=True)
+        workspace = _workspace(workspace, need, dev)
+        st = lib.gdn_linear_prefill_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(cu_seqlens), N, T, Hqk,
+                                             Hv, Dk, Dv, _DTYPE_CODE[q.dtype], float(scale),
+                                             _ptr(initial_state), _ptr(d_o), _ptr(d_final_state), _ptr(dq),
+                                             _ptr(dk), _ptr(dv), _ptr(ds0), _ptr(workspace),
+                                             workspace.numel(), _stream(dev))
+    _check(st, "gdn_linear_prefill_backward")
+    return dq, dk, dv, ds0
 
 
 def linear_decode_tokens(q, k, v, g, state_in, state_out=None, src_slot=None, dst_slot=None, o=None,

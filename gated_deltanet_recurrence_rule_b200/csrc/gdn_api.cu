@@ -56,6 +56,16 @@ cudaError_t launch_backward(const void *q, const void *k, const void *v, const f
                             const float *dO, const float *dSfin, float *dq, float *dk, float *dv,
                             float *dg, float *dbeta, float *ds0, void *workspace,
                             cudaStream_t stream);
+size_t linear_workspace_bytes(int64_t N, int64_t T, int Hqk, int Hv, int Dk, int Dv, bool backward);
+cudaError_t launch_linear_prefill(const void *q, const void *k, const void *v, const float *g,
+                                  const int32_t *cu, int N, int64_t T, int Hqk, int Hv, int Dk, int Dv,
+                                  int dtype, int o_dtype, int state_dtype, float scale, const void *s0,
+                                  void *sf, void *o, void *ws, cudaStream_t stream);
+cudaError_t launch_linear_backward(const void *q, const void *k, const void *v, const float *g,
+                                   const int32_t *cu, int N, int64_t T, int Hqk, int Hv, int Dk, int Dv,
+                                   int dtype, float scale, const float *s0, const void *d_o,
+                                   const float *dsf, void *dq, void *dk, void *dv, float *ds0, void *ws,
+                                   cudaStream_t stream);
 int linear_decode_tokens_max();
 cudaError_t launch_linear_decode(const void *q, const void *k, const void *v, const float *g,
                                  const void *state_in, void *state_out, const int32_t *src_slot,
@@ -369,6 +379,91 @@ int32_t gdn_prefill_backward_sequential(const void *q, const void *k, const void
       q, k, v, g, beta, cu_seqlens, num_seqs, total_tokens, num_qk_heads, num_v_heads, head_dim_k,
       head_dim_v, dtype, scale, initial_state, d_o, d_final_state, dq, dk, dv, dg, dbeta,
       d_initial_state, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+size_t gdn_linear_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens,
+                                         int32_t num_qk_heads, int32_t num_v_heads,
+                                         int32_t head_dim_k, int32_t head_dim_v, int32_t dtype,
+                                         int32_t backward) {
+  if (num_seqs < 0 || total_tokens < 0 || total_tokens > INT32_MAX) return 0;
+  if (!dims_ok(num_qk_heads, num_v_heads, head_dim_k, head_dim_v, dtype)) return 0;
+  if (!dims_supported(head_dim_k, head_dim_v)) return 0;
+  return gdn::linear_workspace_bytes(num_seqs, total_tokens, num_qk_heads, num_v_heads, head_dim_k,
+                                     head_dim_v, backward != 0);
+}
+
+namespace {
+
+// Host checks shared by linear prefill and its backward: GDN_OK to proceed,
+// kNothingToDo, or an error code.
+int32_t check_linear(const void *q, const void *k, const void *v, const float *g,
+                     const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                     int32_t num_qk_heads, int32_t num_v_heads, int32_t head_dim_k,
+                     int32_t head_dim_v, int32_t dtype, const void *workspace,
+                     size_t workspace_bytes, bool backward) {
+  if (num_seqs < 0 || total_tokens < 0 || total_tokens > INT32_MAX) return GDN_ERR_INVALID_ARG;
+  if (!dims_ok(num_qk_heads, num_v_heads, head_dim_k, head_dim_v, dtype)) return GDN_ERR_INVALID_ARG;
+  if (!dims_supported(head_dim_k, head_dim_v)) return GDN_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return total_tokens == 0 ? kNothingToDo : GDN_ERR_INVALID_ARG;
+  if (!cu_seqlens || !aligned(cu_seqlens, 4) || !g || !aligned(g, 4)) return GDN_ERR_INVALID_ARG;
+  if (total_tokens > 0) {
+    if (!q || !k || !v) return GDN_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16)) return GDN_ERR_INVALID_ARG;
+  }
+  // grid-size limits of the launches: 16 tiles of every (segment, head) state, and
+  // a thread for 4 elements of every (token, head) row
+  const int64_t segments = total_tokens / 512 + num_seqs;
+  if (segments * num_v_heads * 16 > INT32_MAX || total_tokens * num_qk_heads / 8 > INT32_MAX)
+    return GDN_ERR_UNSUPPORTED;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < gdn::linear_workspace_bytes(num_seqs, total_tokens, num_qk_heads, num_v_heads,
+                                                    head_dim_k, head_dim_v, backward))
+    return GDN_ERR_WORKSPACE;
+  return GDN_OK;
+}
+
+}  // namespace
+
+int32_t gdn_linear_prefill(const void *q, const void *k, const void *v, const float *g,
+                           const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                           int32_t num_qk_heads, int32_t num_v_heads, int32_t head_dim_k,
+                           int32_t head_dim_v, int32_t dtype, int32_t o_dtype, int32_t state_dtype,
+                           float scale, const void *initial_state, void *final_state, void *o,
+                           void *workspace, size_t workspace_bytes, void *stream) {
+  if (!dtype_ok(o_dtype) || !dtype_ok(state_dtype)) return GDN_ERR_INVALID_ARG;
+  if ((initial_state && !aligned(initial_state, 16)) || (final_state && !aligned(final_state, 16)))
+    return GDN_ERR_INVALID_ARG;
+  if (total_tokens > 0 && (!o || !aligned(o, 16))) return GDN_ERR_INVALID_ARG;
+  const int32_t c = check_linear(q, k, v, g, cu_seqlens, num_seqs, total_tokens, num_qk_heads, num_v_heads,
+                                 head_dim_k, head_dim_v, dtype, workspace, workspace_bytes, false);
+  if (c != GDN_OK) return c == kNothingToDo ? GDN_OK : c;
+  return cuda_status(gdn::launch_linear_prefill(
+      q, k, v, g, cu_seqlens, num_seqs, total_tokens, num_qk_heads, num_v_heads, head_dim_k, head_dim_v,
+      dtype, o_dtype, state_dtype, scale, initial_state, final_state, o, workspace,
+      static_cast<cudaStream_t>(stream)));
+}
+
+int32_t gdn_linear_prefill_backward(const void *q, const void *k, const void *v, const float *g,
+                                    const int32_t *cu_seqlens, int32_t num_seqs,
+                                    int64_t total_tokens, int32_t num_qk_heads, int32_t num_v_heads,
+                                    int32_t head_dim_k, int32_t head_dim_v, int32_t dtype,
+                                    float scale, const float *initial_state, const void *d_o,
+                                    const float *d_final_state, void *dq, void *dk, void *dv,
+                                    float *d_initial_state, void *workspace,
+                                    size_t workspace_bytes, void *stream) {
+  if ((initial_state && !aligned(initial_state, 16)) || (d_final_state && !aligned(d_final_state, 16)) ||
+      (d_initial_state && !aligned(d_initial_state, 16)))
+    return GDN_ERR_INVALID_ARG;
+  if (total_tokens > 0 && (!d_o || !dq || !dk || !dv || !aligned(d_o, 16) || !aligned(dq, 16) ||
+                           !aligned(dk, 16) || !aligned(dv, 16)))
+    return GDN_ERR_INVALID_ARG;
+  const int32_t c = check_linear(q, k, v, g, cu_seqlens, num_seqs, total_tokens, num_qk_heads, num_v_heads,
+                                 head_dim_k, head_dim_v, dtype, workspace, workspace_bytes, true);
+  if (c != GDN_OK) return c == kNothingToDo ? GDN_OK : c;
+  return cuda_status(gdn::launch_linear_backward(
+      q, k, v, g, cu_seqlens, num_seqs, total_tokens, num_qk_heads, num_v_heads, head_dim_k, head_dim_v,
+      dtype, scale, initial_state, d_o, d_final_state, dq, dk, dv, d_initial_state, workspace,
+      static_cast<cudaStream_t>(stream)));
 }
 
 int32_t gdn_linear_decode_tokens(const void *q, const void *k, const void *v, const float *g,

@@ -1,0 +1,547 @@
+// gdn_linear_scan.cu -- linear attention with a decay for each head: the plan and
+// prefix kernels, the scan for every element type and head dim on warp-level tf32
+// MMAs, and the host drivers of prefill and backward.  gdn_linear.cuh has the
+// mathematics; gdn_linear_tc.cu the tcgen05 form of the scan.
+#include <algorithm>
+
+#include "gdn_chunk_ops.cuh"
+#include "gdn_common.cuh"
+#include "gdn_linear.cuh"
+
+namespace gdn {
+namespace lin {
+
+using chunk::mma_tf32_16x8x8;
+using chunk::to_tf32;
+
+// ---------------------------------------------------------------- plan
+// Segment tables of the packed sequences, by one CTA.  Units of unequal length are
+// started longest first, so that the last ones to finish are short; beyond
+// kMaxSorted segments there are enough waves of units for the order not to matter.
+constexpr int kMaxSorted = 512;
+__global__ void __launch_bounds__(1024)
+plan_segments_kernel(const int32_t *__restrict__ cu, int N, int T, int L, int32_t *first_seg,
+                     int32_t *seg_seq, int32_t *order, int32_t *status) {
+  __shared__ int wsum[32], run_s;
+  __shared__ int length[kMaxSorted];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  int bad = 0;
+  for (int i = tid; i <= N; i += 1024) {
+    const int c = cu[i];
+    bad |= c < 0 || c > T || (i == 0 && c != 0) || (i == N && c != T) || (i < N && cu[i + 1] < c);
+  }
+  if (tid == 0) run_s = 0;
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) {
+      report_status(status, GDN_ERR_BAD_SEQLENS);
+      first_seg[N] = -1;
+    }
+    return;
+  }
+  for (int base = 0; base < N; base += 1024) {
+    const int n = base + tid;
+    const int cnt = n < N ? (cu[n + 1] - cu[n] + L - 1) / L : 0;
+    int inc = cnt;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += x;
+    }
+    if (lane == 31) wsum[wid] = inc;
+    __syncthreads();
+    if (wid == 0) {
+      int v = wsum[lane];
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += x;
+      }
+      wsum[lane] = v;
+    }
+    __syncthreads();
+    const int start = run_s + (wid ? wsum[wid - 1] : 0) + inc - cnt;
+    if (n < N) {
+      first_seg[n] = start;
+      for (int i = 0; i < cnt; ++i) {
+        seg_seq[start + i] = n;
+        order[start + i] = start + i;
+        if (start + i < kMaxSorted) length[start + i] = min(L, cu[n + 1] - cu[n] - i * L);
+      }
+    }
+    __syncthreads();
+    if (tid == 0) run_s += wsum[31];
+    __syncthreads();
+  }
+  const int total = run_s;
+  if (tid == 0) first_seg[N] = total;
+  if (total <= kMaxSorted && tid < total) {
+    int rank = 0;
+    for (int i = 0; i < total; ++i) rank += length[i] > length[tid] || (length[i] == length[tid] && i < tid);
+    order[rank] = tid;
+  }
+}
+
+// ---------------------------------------------------------------- prefix
+// Per (sequence of several segments, head): the states that the segments add become
+// the states that they start from, in place (`nat`) and/or transposed (`tr`).  One CTA per 32 x 32 tile of one state: 4 elements a thread.
+struct Prefix {
+  const float *g;
+  const int32_t *cu, *first_seg;
+  int N, Hv, L, Da, Dc, back;
+  float *nat, *tr;
+  int keep_nat;      // the starting states are wanted in nat
+  const void *x0;    // [N, Hv, Dc, Da]
+  void *xf;          // final states: an empty sequence's is its initial one
+  int x_bf16;
+};
+
+__global__ void __launch_bounds__(256) prefix_kernel(const Prefix p) {
+  __shared__ float tile[32][33];
+  if (p.first_seg[p.N] < 0) return;  // inconsistent cu_seqlens
+  const int tiles = (p.Da / 32) * (p.Dc / 32);
+  const int unit = blockIdx.x / tiles, tl = blockIdx.x - unit * tiles;
+  const int n = unit / p.Hv, h = unit - n * p.Hv;
+  const int i0 = 32 * (tl / (p.Da / 32)), j0 = 32 * (tl % (p.Da / 32));
+  const int r = threadIdx.x >> 3, c = 4 * (threadIdx.x & 7);
+  const size_t in_state = (size_t)(i0 + r) * p.Da + j0 + c;
+  const size_t state = (size_t)p.Da * p.Dc;
+  const int s0 = p.first_seg[n], cnt = p.first_seg[n + 1] - s0;
+  const int len = p.cu[n + 1] - p.cu[n];
+  const float gh = fmaxf(p.g[h], -30.f);
+  const size_t e0 = ((size_t)n * p.Hv + h) * state + in_state;
+  float x[4] = {0.f, 0.f, 0.f, 0.f};
+  if (p.x0) load_state4(p.x0, e0, p.x_bf16, x);
+  if (cnt == 0 && p.xf) store_state4(p.xf, e0, p.x_bf16, x);
+  for (int i = 0; i < cnt && cnt > 1; ++i) {
+    const int sg = p.back ? cnt - 1 - i : i;
+    const size_t at = ((size_t)(s0 + sg) * p.Hv + h) * state;
+    float add[4];
+    if (i + 1 < cnt) load4(p.nat + at + in_state, add);  // before its place takes the starting state
+    if (p.keep_nat) *reinterpret_cast<float4 *>(p.nat + at + in_state) = make_float4(x[0], x[1], x[2], x[3]);
+    if (p.tr) {
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tile[c + k][r] = x[k];
+      __syncthreads();
+      *reinterpret_cast<float4 *>(p.tr + at + (size_t)(j0 + r) * p.Dc + i0 + c) =
+          make_float4(tile[r][c], tile[r][c + 1], tile[r][c + 2], tile[r][c + 3]);
+    }
+    if (i + 1 == cnt) break;
+    const int tokens = min(p.L, len - sg * p.L) - (p.back && i == 0 ? 1 : 0);
+    const float f = expf(gh * (float)tokens);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = fmaf(f, x[k], add[k]);
+  }
+}
+
+// ---------------------------------------------------------------- the scan
+// d += A (16 x 8) B (8 x 8) in tf32 with the operands split in two terms (three
+// products, about fp32) where they are not exact in tf32 (EXA, EXB: bf16 inputs).
+template <bool EXA, bool EXB>
+__device__ __forceinline__ void mma_split(float *d, const float *a, const float *b) {
+  uint32_t ah[4], bh[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) ah[i] = to_tf32(a[i]);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) bh[i] = to_tf32(b[i]);
+  if (!EXB) {
+    const uint32_t bl[2] = {to_tf32(b[0] - __uint_as_float(bh[0])), to_tf32(b[1] - __uint_as_float(bh[1]))};
+    mma_tf32_16x8x8(d, ah, bl);
+  }
+  if (!EXA) {
+    const uint32_t al[4] = {to_tf32(a[0] - __uint_as_float(ah[0])), to_tf32(a[1] - __uint_as_float(ah[1])),
+                            to_tf32(a[2] - __uint_as_float(ah[2])), to_tf32(a[3] - __uint_as_float(ah[3]))};
+    mma_tf32_16x8x8(d, al, bh);
+  }
+  mma_tf32_16x8x8(d, ah, bh);
+}
+
+constexpr int C = 64;    // chunk length
+constexpr int DCT = 64;  // columns of out (rows of X) of one CTA
+
+template <int DA>
+struct Smem {
+  float a[C][DA + 4], b[C][DA + 4], c[C][DCT + 8], P[C][C + 4], X[DCT][DA + 4], pw[C + 1];
+};
+
+// One CTA per (segment, head, 64 columns of out), 8 warps.  Per chunk of 64
+// tokens: P = (A B^T) . lam^{|t-s|}; out = s_intra P C + s_inter lam^{p+1} A X^T;
+// X <- lam^len X + (w C)^T B.  X stays in fp32 accumulator registers, with a copy
+// in shared memory as an operand.  Bound: the tf32 products (three for each fp32
+// one).  This form serves fp32 inputs, fp32 outputs and head dim 64.
+template <typename T, typename TO, int DA, bool OUT>
+__global__ void __launch_bounds__(256) scan_kernel(const Scan p) {
+  constexpr bool EX = sizeof(T) == 2;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  Smem<DA> &s = *reinterpret_cast<Smem<DA> *>(smem_raw);
+  const int splits = p.Dc / DCT;
+  const int unit = blockIdx.x / splits, dc0 = DCT * (blockIdx.x - unit * splits);
+  Unit w;
+  if (!get_unit(p, unit, w)) return;
+  if (!OUT && w.last) return;  // no segment starts from its end
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
+  const int ha = w.h / (p.Hv / p.Ha), hb = w.h / (p.Hv / p.Hb), hc = w.h / (p.Hv / p.Hc);
+  const float gh = head_decay(p, w.h);
+  if (tid <= C) s.pw[tid] = expf(gh * (float)tid);
+  const int mt = warp >> 1, nh = warp & 1;  // this warp's 16 rows and half of the columns
+  constexpr int NX = DA / 16;               // 8-column tiles of X per warp
+
+  float X[NX][4];
+  if (OUT) {
+#pragma unroll
+    for (int n = 0; n < NX; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        X[n][e] = start_state(p, w, dc0 + 16 * mt + gid + 8 * (e >> 1), 8 * (nh * NX + n) + 2 * tig + (e & 1));
+  } else {
+#pragma unroll
+    for (int n = 0; n < NX; ++n) X[n][0] = X[n][1] = X[n][2] = X[n][3] = 0.f;
+  }
+  auto put_x = [&]() {
+#pragma unroll
+    for (int n = 0; n < NX; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        s.X[16 * mt + gid + 8 * (e >> 1)][8 * (nh * NX + n) + 2 * tig + (e & 1)] = X[n][e];
+  };
+  if (OUT) put_x();
+
+  const int nch = (w.t1 - w.t0 + C - 1) / C;
+  for (int ci = 0; ci < nch; ++ci) {
+    const int c = p.back ? nch - 1 - ci : ci;
+    const int t0 = w.t0 + c * C, len = min(C, w.t1 - t0);
+    const int skip = p.back && w.first && ci == 0 ? 1 : 0;
+    __syncthreads();  // the last chunk's tiles have been used
+    auto load = [&](const void *base, int H, int h, int D, int d0, int width, float *dst, int ld) {
+      for (int x = tid; x < C * width / 4; x += 256) {
+        const int r = x / (width / 4), d = 4 * (x - r * (width / 4));
+        float y[4] = {0.f, 0.f, 0.f, 0.f};  // rows past the segment read as zeros
+        if (r < len) load4(static_cast<const T *>(base) + ((size_t)(t0 + r) * H + h) * D + d0 + d, y);
+        *reinterpret_cast<float4 *>(dst + r * ld + d) = make_float4(y[0], y[1], y[2], y[3]);
+      }
+    };
+    if (OUT) load(p.a, p.Ha, ha, DA, 0, DA, &s.a[0][0], DA + 4);
+    load(p.b, p.Hb, hb, DA, 0, DA, &s.b[0][0], DA + 4);
+    load(p.c, p.Hc, hc, p.Dc, dc0, DCT, &s.c[0][0], DCT + 8);
+    __syncthreads();
+    if (OUT) {
+      // P, rows t of tile mt, columns s of half nh
+      float acc[4][4] = {};
+#pragma unroll 2
+      for (int k = 0; k < DA; k += 8) {
+        const float af[4] = {s.a[16 * mt + gid][k + tig], s.a[16 * mt + gid + 8][k + tig],
+                             s.a[16 * mt + gid][k + tig + 4], s.a[16 * mt + gid + 8][k + tig + 4]};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int sc = 8 * (4 * nh + n) + gid;
+          const float bf[2] = {s.b[sc][k + tig], s.b[sc][k + tig + 4]};
+          mma_split<EX, EX>(acc[n], af, bf);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = 16 * mt + gid + 8 * (e >> 1), sc = 8 * (4 * nh + n) + 2 * tig + (e & 1);
+          const int d = p.back ? sc - t : t - sc;
+          s.P[t][sc] = d >= 0 ? acc[n][e] * s.pw[d] : 0.f;
+        }
+      __syncthreads();
+      float oi[4][4] = {}, oa[4][4] = {};
+#pragma unroll 2
+      for (int k = 0; k < DA; k += 8) {
+        const float af[4] = {s.a[16 * mt + gid][k + tig], s.a[16 * mt + gid + 8][k + tig],
+                             s.a[16 * mt + gid][k + tig + 4], s.a[16 * mt + gid + 8][k + tig + 4]};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int dc = 8 * (4 * nh + n) + gid;
+          const float bf[2] = {s.X[dc][k + tig], s.X[dc][k + tig + 4]};
+          mma_split<EX, false>(oi[n], af, bf);
+        }
+      }
+#pragma unroll 2
+      for (int k = 0; k < C; k += 8) {
+        const float af[4] = {s.P[16 * mt + gid][k + tig], s.P[16 * mt + gid + 8][k + tig],
+                             s.P[16 * mt + gid][k + tig + 4], s.P[16 * mt + gid + 8][k + tig + 4]};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int dc = 8 * (4 * nh + n) + gid;
+          const float bf[2] = {s.c[k + tig][dc], s.c[k + tig + 4][dc]};
+          mma_split<false, EX>(oa[n], af, bf);
+        }
+      }
+      TO *out = static_cast<TO *>(p.out);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int t = 16 * mt + gid + 8 * r;
+        if (t >= len) continue;
+        const float wi = p.s_inter * s.pw[(p.back ? len - 1 - t : t) + 1 - skip];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          TO *o = out + ((size_t)(t0 + t) * p.Hv + w.h) * p.Dc + dc0 + 8 * (4 * nh + n) + 2 * tig;
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            o[e] = from_f32<TO>(fmaf(wi, oi[n][2 * r + e], p.s_intra * oa[n][2 * r + e]));
+        }
+      }
+    }
+    // X <- lam^len X + sum_t (s_upd lam^{rest} c_t) b_t^T
+    // (the chunk's sum on its own: tensor cores cut what an addition shifts out, which
+    // over many additions to a large X would be a drift)
+    float dx[NX][4] = {};
+#pragma unroll 2
+    for (int k = 0; k < C; k += 8) {
+      float wt[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = k + tig + 4 * i, rest = p.back ? t : len - 1 - t;
+        wt[i] = t < len ? p.s_upd * s.pw[rest] : 0.f;
+      }
+      const float af[4] = {wt[0] * s.c[k + tig][16 * mt + gid], wt[0] * s.c[k + tig][16 * mt + gid + 8],
+                           wt[1] * s.c[k + tig + 4][16 * mt + gid], wt[1] * s.c[k + tig + 4][16 * mt + gid + 8]};
+#pragma unroll
+      for (int n = 0; n < NX; ++n) {
+        const int da = 8 * (nh * NX + n) + gid;
+        const float bf[2] = {s.b[k + tig][da], s.b[k + tig + 4][da]};
+        mma_split<false, EX>(dx[n], af, bf);
+      }
+    }
+    const float lx = s.pw[len - skip];
+#pragma unroll
+    for (int n = 0; n < NX; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) X[n][e] = fmaf(lx, X[n][e], dx[n][e]);
+    if (OUT) {
+      __syncthreads();  // X has been used
+      put_x();
+    }
+  }
+  const bool fin = OUT && w.last && p.xf;
+  if (OUT && !fin) return;
+  const float f = fin && p.back && nch > 0 ? expf(gh) : 1.f;
+  const size_t base = fin ? ((size_t)w.n * p.Hv + w.h) * p.Dc * p.Da
+                          : ((size_t)w.seg * p.Hv + w.h) * p.Dc * p.Da;
+#pragma unroll
+  for (int n = 0; n < NX; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const size_t at = base + (size_t)(dc0 + 16 * mt + gid + 8 * (e >> 1)) * p.Da +
+                        8 * (nh * NX + n) + 2 * tig + (e & 1);
+      if (fin && p.x_bf16) static_cast<__nv_bfloat16 *>(p.xf)[at] = __float2bfloat16_rn(f * X[n][e]);
+      else (fin ? static_cast<float *>(p.xf) : p.seg_state)[at] = f * X[n][e];
+    }
+}
+
+template <typename T, typename TO, int DA>
+static cudaError_t launch_scan_t(const Scan &p, int units, cudaStream_t stream) {
+  static std::atomic<bool> f0[64], f1[64];
+  constexpr int bytes = (int)sizeof(Smem<DA>);
+  static_assert(bytes <= 232448, "shared memory of a CTA");
+  const unsigned grid = (unsigned)units * (unsigned)(p.Dc / DCT);
+  cudaError_t e;
+  if (p.out) {
+    if ((e = set_smem_once(scan_kernel<T, TO, DA, true>, bytes, f1)) != cudaSuccess) return e;
+    scan_kernel<T, TO, DA, true><<<grid, 256, bytes, stream>>>(p);
+  } else {
+    if ((e = set_smem_once(scan_kernel<T, T, DA, false>, bytes, f0)) != cudaSuccess) return e;
+    scan_kernel<T, T, DA, false><<<grid, 256, bytes, stream>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_scan(const Scan &p, int units, int dtype, int out_dtype, cudaStream_t stream) {
+  return dispatch_types(dtype, out_dtype, [&](auto t, auto to) {
+    using T = decltype(t);
+    using TO = decltype(to);
+    if (p.Da == 128) return launch_scan_t<T, TO, 128>(p, units, stream);
+    return launch_scan_t<T, TO, 64>(p, units, stream);
+  });
+}
+
+// ---------------------------------------------------------------- group sums
+// out[t, j] = sum over the G value heads of query/key head j of part[t, jG + r]
+// (fp32 partials, summed in order, rounded once).  4 columns a thread.
+template <typename TO>
+__global__ void __launch_bounds__(256)
+group_sum_kernel(const float *__restrict__ part, TO *__restrict__ out, size_t quads, int D, int G) {
+  const size_t x = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (x >= quads) return;
+  const size_t row = x / (D / 4), d = 4 * (x - row * (D / 4));
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int r = 0; r < G; ++r) {
+    const float4 y = __ldcs(reinterpret_cast<const float4 *>(part + (row * G + r) * D + d));
+    s[0] += y.x; s[1] += y.y; s[2] += y.z; s[3] += y.w;
+  }
+  store_state4(out, row * D + d, sizeof(TO) == 2, s);
+}
+
+// ---------------------------------------------------------------- host drivers
+namespace {
+
+size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Segment length in tokens (a multiple of 128, the longest chunk): the share of one
+// multiprocessor, so that a single sequence makes one wave of units and only a
+// sequence longer than that share is cut (the cut costs a second reading of b and c).
+int segment_len(int64_t T, int Hv) {
+  const int64_t units = std::max<int64_t>(1, sm_count() / Hv);  // segments of one wave
+  return (int)std::max<int64_t>(512, round_up((size_t)((T + units - 1) / units), 128));
+}
+
+struct Layout {
+  int L;
+  int64_t max_seg;
+  size_t first_seg, seg_seq, order, nat, tr, part, total;
+};
+
+Layout layout(int64_t N, int64_t T, int Hqk, int Hv, int Dk, int Dv, bool backward) {
+  Layout l;
+  l.L = segment_len(T, Hv);
+  const bool one = T <= l.L;
+  l.max_seg = one ? N : T / l.L + N;
+  size_t at = kWorkspaceHeaderBytes;
+  l.first_seg = at;
+  if (!one) at = round_up(at + sizeof(int32_t) * (size_t)(N + 1), 256);
+  l.seg_seq = at;
+  if (!one) at = round_up(at + sizeof(int32_t) * (size_t)l.max_seg, 256);
+  l.order = at;
+  if (!one) at = round_up(at + sizeof(int32_t) * (size_t)l.max_seg, 1024);
+  const size_t states = one ? 0 : round_up((size_t)l.max_seg * Hv * Dk * Dv * sizeof(float), 1024);
+  l.nat = at;
+  at += states;
+  l.tr = at;
+  if (backward) at += states;
+  l.part = at;
+  if (backward && Hv > Hqk) at = round_up(at + (size_t)T * Hv * Dk * sizeof(float), 1024);
+  l.total = at;
+  return l;
+}
+
+}  // namespace
+}  // namespace lin
+
+size_t linear_workspace_bytes(int64_t N, int64_t T, int Hqk, int Hv, int Dk, int Dv, bool backward) {
+  return lin::layout(N, T, Hqk, Hv, Dk, Dv, backward).total;
+}
+
+namespace lin {
+
+static cudaError_t run_scan(const Scan &p, int units, int dtype, int out_dtype, cudaStream_t stream) {
+  return launch_scan(p, units, dtype, out_dtype, stream);
+}
+
+// Plan the segments and point `p` at the tables.
+static cudaError_t run_plan(Scan &p, const Layout &l, unsigned char *ws, cudaStream_t stream) {
+  int32_t *first_seg = reinterpret_cast<int32_t *>(ws + l.first_seg);
+  int32_t *seg_seq = reinterpret_cast<int32_t *>(ws + l.seg_seq);
+  int32_t *order = reinterpret_cast<int32_t *>(ws + l.order);
+  plan_segments_kernel<<<1, 1024, 0, stream>>>(p.cu, p.N, p.T, l.L, first_seg, seg_seq, order, p.status);
+  p.first_seg = first_seg;
+  p.seg_seq = seg_seq;
+  p.order = order;
+  return cudaGetLastError();
+}
+
+static cudaError_t run_prefix(const Prefix &p, cudaStream_t stream) {
+  const unsigned grid = (unsigned)p.N * (unsigned)p.Hv * (unsigned)((p.Da / 32) * (p.Dc / 32));
+  prefix_kernel<<<grid, 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace lin
+
+cudaError_t launch_linear_prefill(const void *q, const void *k, const void *v, const float *g,
+                                  const int32_t *cu, int N, int64_t T, int Hqk, int Hv, int Dk, int Dv,
+                                  int dtype, int o_dtype, int state_dtype, float scale, const void *s0,
+                                  void *sf, void *o, void *ws, cudaStream_t stream) {
+  using namespace lin;
+  const lin::Layout l = layout(N, T, Hqk, Hv, Dk, Dv, false);
+  unsigned char *w = static_cast<unsigned char *>(ws);
+  Scan p = {};
+  p.a = q; p.b = k; p.c = v; p.Ha = p.Hb = Hqk; p.Hc = Hv; p.g = g; p.cu = cu; p.N = N; p.T = (int)T;
+  p.Hv = Hv; p.Da = Dk; p.Dc = Dv; p.s_intra = p.s_inter = scale; p.s_upd = 1.f; p.L = l.L;
+  p.status = static_cast<int32_t *>(ws);
+  p.x0 = s0; p.xf = sf; p.x_bf16 = state_dtype == GDN_DTYPE_BF16;
+  if (T <= l.L) {
+    p.out = o;
+    return run_scan(p, N * Hv, dtype, o_dtype, stream);
+  }
+  cudaError_t e = run_plan(p, l, w, stream);
+  if (e != cudaSuccess) return e;
+  p.seg_state = reinterpret_cast<float *>(w + l.nat);
+  const int units = (int)l.max_seg * Hv;
+  if ((e = run_scan(p, units, dtype, dtype, stream)) != cudaSuccess) return e;  // out NULL: states
+  Prefix x = {};
+  x.g = g; x.cu = cu; x.first_seg = p.first_seg; x.N = N; x.Hv = Hv; x.L = l.L; x.Da = Dk; x.Dc = Dv;
+  x.nat = p.seg_state; x.keep_nat = 1; x.x0 = s0; x.xf = sf; x.x_bf16 = p.x_bf16;
+  if ((e = run_prefix(x, stream)) != cudaSuccess) return e;
+  p.out = o;
+  return run_scan(p, units, dtype, o_dtype, stream);
+}
+
+cudaError_t launch_linear_backward(const void *q, const void *k, const void *v, const float *g,
+                                   const int32_t *cu, int N, int64_t T, int Hqk, int Hv, int Dk, int Dv,
+                                   int dtype, float scale, const float *s0, const void *d_o,
+                                   const float *dsf, void *dq, void *dk, void *dv, float *ds0, void *ws,
+                                   cudaStream_t stream) {
+  using namespace lin;
+  const lin::Layout l = layout(N, T, Hqk, Hv, Dk, Dv, true);
+  unsigned char *w = static_cast<unsigned char *>(ws);
+  const bool one = T <= l.L, grouped = Hv > Hqk;
+  Scan base = {};
+  base.g = g; base.cu = cu; base.N = N; base.T = (int)T; base.Hv = Hv; base.L = l.L;
+  base.status = static_cast<int32_t *>(ws);
+  float *nat = reinterpret_cast<float *>(w + l.nat), *tr = reinterpret_cast<float *>(w + l.tr);
+  float *part = reinterpret_cast<float *>(w + l.part);
+  const int units = (int)l.max_seg * Hv;
+  cudaError_t e = cudaSuccess;
+  if (!one && (e = run_plan(base, l, w, stream)) != cudaSuccess) return e;
+  Prefix x = {};
+  x.g = g; x.cu = cu; x.first_seg = base.first_seg; x.N = N; x.Hv = Hv; x.L = l.L; x.Da = Dk; x.Dc = Dv;
+  x.nat = nat; x.tr = tr;
+
+  // dq (and dk) of a query/key head: fp32 partials of its value heads, then their sum
+  auto into = [&](Scan p, void *out) -> cudaError_t {
+    p.out = grouped ? part : out;
+    cudaError_t r = run_scan(p, units, dtype, grouped ? GDN_DTYPE_FP32 : dtype, stream);
+    if (r != cudaSuccess || !grouped) return r;
+    const size_t quads = (size_t)T * Hqk * Dk / 4;
+    const unsigned blocks = (unsigned)((quads + 255) / 256);
+    if (dtype == GDN_DTYPE_BF16)
+      group_sum_kernel<<<blocks, 256, 0, stream>>>(part, static_cast<__nv_bfloat16 *>(out), quads, Dk, Hv / Hqk);
+    else
+      group_sum_kernel<<<blocks, 256, 0, stream>>>(part, static_cast<float *>(out), quads, Dk, Hv / Hqk);
+    return cudaGetLastError();
+  };
+
+  Scan p = base;  // S, for dq
+  p.a = q; p.Ha = Hqk; p.b = k; p.Hb = Hqk; p.c = v; p.Hc = Hv; p.Da = Dk; p.Dc = Dv; p.s_upd = 1.f;
+  if (!one) {
+    p.seg_state = nat;
+    if ((e = run_scan(p, units, dtype, dtype, stream)) != cudaSuccess) return e;
+    x.x0 = s0; x.back = 0; x.keep_nat = 0;
+    if ((e = run_prefix(x, stream)) != cudaSuccess) return e;
+  }
+  p = base;
+  p.a = d_o; p.Ha = Hv; p.b = v; p.Hb = Hv; p.c = k; p.Hc = Hqk; p.Da = Dv; p.Dc = Dk;
+  p.s_intra = p.s_inter = scale; p.s_upd = 1.f; p.seg_state = tr; p.x0 = s0; p.x0_tr = 1;
+  if ((e = into(p, dq)) != cudaSuccess) return e;
+
+  p = base;  // D, for dv and dk
+  p.back = 1;
+  p.a = k; p.Ha = Hqk; p.b = q; p.Hb = Hqk; p.c = d_o; p.Hc = Hv; p.Da = Dk; p.Dc = Dv;
+  p.s_intra = p.s_upd = scale; p.s_inter = 1.f; p.seg_state = nat; p.x0 = dsf;
+  if (!one) {
+    if ((e = run_scan(p, units, dtype, dtype, stream)) != cudaSuccess) return e;
+    x.x0 = dsf; x.back = 1; x.keep_nat = 1; x.xf = ds0;
+    if ((e = run_prefix(x, stream)) != cudaSuccess) return e;
+  }
+  p.out = dv;
+  p.xf = ds0;
+  if ((e = run_scan(p, units, dtype, dtype, stream)) != cudaSuccess) return e;
+  p.a = v; p.Ha = Hv; p.b = d_o; p.Hb = Hv; p.c = q; p.Hc = Hqk; p.Da = Dv; p.Dc = Dk;
+  p.seg_state = tr; p.x0_tr = 1; p.xf = nullptr;
+  return into(p, dk);
+}
+
+}  // namespace gdn

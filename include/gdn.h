@@ -426,6 +426,66 @@ int32_t gdn_prefill_backward_sequential(const void *q, const void *k, const void
  * lam = 0) are taken as -30: e^-30 is below the resolution of an fp32 sum.  (The
  * pages describe the gated rule only; this is its relative without the erase.)
  *
+ * gdn_linear_prefill_workspace_size: bytes of device workspace that
+ * gdn_linear_prefill (backward = 0) or gdn_linear_prefill_backward (1) needs (0
+ * for invalid sizes): the status header, and for inputs longer than one
+ * multiprocessor's share the segment tables and one starting state per (segment,
+ * value head); for the backward also the transposed states and, where Hv > Hqk,
+ * an fp32 [T, Hv, Dk] buffer of per-value-head dq or dk.
+ */
+size_t gdn_linear_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens,
+                                         int32_t num_qk_heads, int32_t num_v_heads,
+                                         int32_t head_dim_k, int32_t head_dim_v, int32_t dtype,
+                                         int32_t backward);
+
+/*
+ * Linear attention over num_seqs packed sequences, chunked.  Arguments as for
+ * gdn_prefill, without beta and input_form and with g [Hv].  The workspace must
+ * hold gdn_linear_prefill_workspace_size bytes (GDN_ERR_WORKSPACE otherwise);
+ * 256-byte aligned, zero-filled once; its first word is the sticky status word
+ * (gdn_get_device_status), its second the limit of bounded waits, as there.
+ *
+ * bf16 inputs and bf16 o at head dim 128 run on the tensor cores (tcgen05), with
+ * the state in fp32 and its increments from products exact to fp32; the state and
+ * the token x token products are rounded to bf16 once, as operands of o, which is
+ * itself rounded to bf16.  Everything else runs on warp-level tf32 MMAs with split
+ * operands, at about fp32 accuracy.  Rows past a sequence's end are neither read
+ * into its results nor written.
+ */
+int32_t gdn_linear_prefill(const void *q, const void *k, const void *v, const float *g,
+                           const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                           int32_t num_qk_heads, int32_t num_v_heads, int32_t head_dim_k,
+                           int32_t head_dim_v, int32_t dtype, int32_t o_dtype, int32_t state_dtype,
+                           float scale, const void *initial_state, void *final_state, void *o,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Backward pass of gdn_linear_prefill (training): gradients of a loss with respect
+ * to q, k, v and the initial state, given d_o and optionally d_final_state; g is a
+ * constant of the layer and has none.  With D_t = lam D_{t+1} + scale d_o_t q_t^T
+ * going backwards from dL/dS_final,
+ *     dq_t = scale S_t^T d_o_t,  dk_t = D_t^T v_t,  dv_t = D_t k_t,
+ *     d_initial_state = lam D_1,
+ * three scans of the forward's kind.  Training keeps the inputs' precision: d_o,
+ * dq, dk and dv have q's element type (dtype), the states are fp32.
+ *
+ *   d_o [T, Hv, Dv], dq, dk [T, Hqk, Dk], dv [T, Hv, Dv]   dtype
+ *   initial_state, d_final_state   [num_seqs, Hv, Dv, Dk] fp32, or NULL for zeros
+ *   d_initial_state                the same shape, or NULL to skip
+ * dq and dk of a query/key head sum over its value heads in a fixed order in fp32
+ * (results do not depend on scheduling).  The call is stream-ordered and can be
+ * captured in a CUDA graph.
+ */
+int32_t gdn_linear_prefill_backward(const void *q, const void *k, const void *v, const float *g,
+                                    const int32_t *cu_seqlens, int32_t num_seqs,
+                                    int64_t total_tokens, int32_t num_qk_heads, int32_t num_v_heads,
+                                    int32_t head_dim_k, int32_t head_dim_v, int32_t dtype,
+                                    float scale, const float *initial_state, const void *d_o,
+                                    const float *d_final_state, void *dq, void *dk, void *dv,
+                                    float *d_initial_state, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/*
  * gdn_linear_decode_tokens: `tokens` new tokens for each of `batch` sequences
  * against a pool of states.  Arguments, slots, padding entries and errors as in
  * gdn_decode_tokens, without beta and input_form, and with g [Hv].
