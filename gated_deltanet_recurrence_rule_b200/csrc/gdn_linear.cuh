@@ -102,9 +102,11 @@ __device__ __forceinline__ float start_state(const Scan &p, const Unit &w, int i
 // ---- host ----
 // The CUDA-core-and-mma.sync form, every type and head dim (gdn_linear_scan.cu).
 cudaError_t launch_scan(const Scan &p, int units, int dtype, int out_dtype, cudaStream_t stream);
-// The tcgen05 form (gdn_linear_tc.cu): bf16 operands and output, Da = Dc = 128.
-bool scan_tc_supported(int Da, int Dc, int dtype, int out_dtype);
-cudaError_t launch_scan_tc(const Scan &p, int units, cudaStream_t stream);
+// The tcgen05 form (gdn_linear_tc.cu): bf16 operands, Da = Dc = 128.  Its states
+// are exact to fp32; its outputs carry the roundings of bf16 operands, whatever type
+// they are stored in.
+bool scan_tc_supported(const Scan &p, int dtype);
+cudaError_t launch_scan_tc(const Scan &p, int units, int out_dtype, cudaStream_t stream);
 
 }  // namespace lin
 }  // namespace gdn

@@ -426,7 +426,12 @@ size_t linear_workspace_bytes(int64_t N, int64_t T, int Hqk, int Hv, int Dk, int
 
 namespace lin {
 
-static cudaError_t run_scan(const Scan &p, int units, int dtype, int out_dtype, cudaStream_t stream) {
+// result_dtype: the type the caller's result ends up in.  Where that is bf16 (or
+// only states are wanted) the tcgen05 form serves.
+static cudaError_t run_scan(const Scan &p, int units, int dtype, int out_dtype, int result_dtype,
+                            cudaStream_t stream) {
+  if ((!p.out || result_dtype == GDN_DTYPE_BF16) && scan_tc_supported(p, dtype))
+    return launch_scan_tc(p, units, out_dtype, stream);
   return launch_scan(p, units, dtype, out_dtype, stream);
 }
 
@@ -464,19 +469,19 @@ cudaError_t launch_linear_prefill(const void *q, const void *k, const void *v, c
   p.x0 = s0; p.xf = sf; p.x_bf16 = state_dtype == GDN_DTYPE_BF16;
   if (T <= l.L) {
     p.out = o;
-    return run_scan(p, N * Hv, dtype, o_dtype, stream);
+    return run_scan(p, N * Hv, dtype, o_dtype, o_dtype, stream);
   }
   cudaError_t e = run_plan(p, l, w, stream);
   if (e != cudaSuccess) return e;
   p.seg_state = reinterpret_cast<float *>(w + l.nat);
   const int units = (int)l.max_seg * Hv;
-  if ((e = run_scan(p, units, dtype, dtype, stream)) != cudaSuccess) return e;  // out NULL: states
+  if ((e = run_scan(p, units, dtype, dtype, dtype, stream)) != cudaSuccess) return e;  // out NULL: states
   Prefix x = {};
   x.g = g; x.cu = cu; x.first_seg = p.first_seg; x.N = N; x.Hv = Hv; x.L = l.L; x.Da = Dk; x.Dc = Dv;
   x.nat = p.seg_state; x.keep_nat = 1; x.x0 = s0; x.xf = sf; x.x_bf16 = p.x_bf16;
   if ((e = run_prefix(x, stream)) != cudaSuccess) return e;
   p.out = o;
-  return run_scan(p, units, dtype, o_dtype, stream);
+  return run_scan(p, units, dtype, o_dtype, o_dtype, stream);
 }
 
 cudaError_t launch_linear_backward(const void *q, const void *k, const void *v, const float *g,
@@ -503,7 +508,7 @@ cudaError_t launch_linear_backward(const void *q, const void *k, const void *v, 
   // dq (and dk) of a query/key head: fp32 partials of its value heads, then their sum
   auto into = [&](Scan p, void *out) -> cudaError_t {
     p.out = grouped ? part : out;
-    cudaError_t r = run_scan(p, units, dtype, grouped ? GDN_DTYPE_FP32 : dtype, stream);
+    cudaError_t r = run_scan(p, units, dtype, grouped ? GDN_DTYPE_FP32 : dtype, dtype, stream);
     if (r != cudaSuccess || !grouped) return r;
     const size_t quads = (size_t)T * Hqk * Dk / 4;
     const unsigned blocks = (unsigned)((quads + 255) / 256);
@@ -518,7 +523,7 @@ cudaError_t launch_linear_backward(const void *q, const void *k, const void *v, 
   p.a = q; p.Ha = Hqk; p.b = k; p.Hb = Hqk; p.c = v; p.Hc = Hv; p.Da = Dk; p.Dc = Dv; p.s_upd = 1.f;
   if (!one) {
     p.seg_state = nat;
-    if ((e = run_scan(p, units, dtype, dtype, stream)) != cudaSuccess) return e;
+    if ((e = run_scan(p, units, dtype, dtype, dtype, stream)) != cudaSuccess) return e;
     x.x0 = s0; x.back = 0; x.keep_nat = 0;
     if ((e = run_prefix(x, stream)) != cudaSuccess) return e;
   }
@@ -532,13 +537,13 @@ cudaError_t launch_linear_backward(const void *q, const void *k, const void *v, 
   p.a = k; p.Ha = Hqk; p.b = q; p.Hb = Hqk; p.c = d_o; p.Hc = Hv; p.Da = Dk; p.Dc = Dv;
   p.s_intra = p.s_upd = scale; p.s_inter = 1.f; p.seg_state = nat; p.x0 = dsf;
   if (!one) {
-    if ((e = run_scan(p, units, dtype, dtype, stream)) != cudaSuccess) return e;
+    if ((e = run_scan(p, units, dtype, dtype, dtype, stream)) != cudaSuccess) return e;
     x.x0 = dsf; x.back = 1; x.keep_nat = 1; x.xf = ds0;
     if ((e = run_prefix(x, stream)) != cudaSuccess) return e;
   }
   p.out = dv;
   p.xf = ds0;
-  if ((e = run_scan(p, units, dtype, dtype, stream)) != cudaSuccess) return e;
+  if ((e = run_scan(p, units, dtype, dtype, dtype, stream)) != cudaSuccess) return e;
   p.a = v; p.Ha = Hv; p.b = d_o; p.Hb = Hv; p.c = q; p.Hc = Hqk; p.Da = Dv; p.Dc = Dk;
   p.seg_state = tr; p.x0_tr = 1; p.xf = nullptr;
   return into(p, dk);
