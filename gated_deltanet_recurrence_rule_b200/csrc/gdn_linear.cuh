@@ -89,14 +89,36 @@ __device__ __forceinline__ bool get_unit(const Scan &p, int u, Unit &w) {
 // A decay below e^-30 is taken as e^-30 (gdn_rows.cuh says why).
 __device__ __forceinline__ float head_decay(const Scan &p, int h) { return fmaxf(p.g[h], -30.f); }
 
-// Element (i, j) of the state a unit starts from.
-__device__ __forceinline__ float start_state(const Scan &p, const Unit &w, int i, int j) {
-  if (!w.first || !w.last) return p.seg_state[(((size_t)w.seg * p.Hv + w.h) * p.Dc + i) * p.Da + j];
+// Element (i, j) of a sequence's initial state.
+__device__ __forceinline__ float initial_state(const Scan &p, const Unit &w, int i, int j) {
   if (!p.x0) return 0.f;
   const size_t base = ((size_t)w.n * p.Hv + w.h) * p.Dc * p.Da;
   const size_t e = base + (p.x0_tr ? (size_t)j * p.Dc + i : (size_t)i * p.Da + j);
   return p.x_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.x0)[e])
                   : static_cast<const float *>(p.x0)[e];
+}
+
+// Element (i, j) of the state a unit starts from.
+__device__ __forceinline__ float start_state(const Scan &p, const Unit &w, int i, int j) {
+  if (!w.first || !w.last) return p.seg_state[(((size_t)w.seg * p.Hv + w.h) * p.Dc + i) * p.Da + j];
+  return initial_state(p, w, i, j);
+}
+
+// W consecutive elements of row i of it (j a multiple of 4).
+template <int W>
+__device__ __forceinline__ void load_start(const Scan &p, const Unit &w, float, int i, int j, float *x) {
+  if (!w.first || !w.last) {
+    const float *s = p.seg_state + (((size_t)w.seg * p.Hv + w.h) * p.Dc + i) * p.Da + j;
+#pragma unroll
+    for (int k = 0; k < W; k += 4) load4(s + k, x + k);
+  } else if (p.x0 && !p.x0_tr) {
+    const size_t e = (((size_t)w.n * p.Hv + w.h) * p.Dc + i) * p.Da + j;
+#pragma unroll
+    for (int k = 0; k < W; k += 4) load_state4(p.x0, e + k, p.x_bf16, x + k);
+  } else {
+#pragma unroll
+    for (int k = 0; k < W; ++k) x[k] = initial_state(p, w, i, j + k);
+  }
 }
 
 // ---- host ----

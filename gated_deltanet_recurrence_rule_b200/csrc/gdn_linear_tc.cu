@@ -9,9 +9,11 @@
 //     dX = (w C)^T B                 w_t = s_upd lam^{rest}
 //     out_t = s_inter lam^{p+1} Oi_t + s_intra Oa_t,   X <- lam^len X + dX.
 // Precision.  A, B, C are exact bf16.  The state is fp32 in registers; w C enters dX
-// as three bf16 terms (24 bits: exact to fp32), each chunk's dX is summed apart and
-// added once, rounded to nearest.  P . lam^{..} and X are rounded to bf16 once as
-// operands of the output, whose own rounding to bf16 is as large.
+// as bf16 terms cut from its fp32 value, 8 bits each: three (all 24 bits) where the
+// state is returned or handed to another segment, two where it only serves outputs;
+// each chunk's dX is summed apart and added once, rounded to nearest.  P . lam^{..}
+// and X are rounded to bf16 once as operands of the output, whose own rounding to
+// bf16 is as large.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -30,7 +32,8 @@ using chunk::CTL_LIMIT;
 namespace {
 
 constexpr int CH = 128, HD = 128;
-constexpr int NTHREADS = 640;  // warp 0 TMA, warp 1 MMA, warp 2 wait limit, warps 4-19 epilogue
+constexpr int NTHREADS = 640;   // states: warp 0 TMA, 1 MMA, 2 wait limit, 4-19 elementwise
+constexpr int NTHREADS_O = 768; // outputs: warp 0 TMA, 1 and 3 MMA, 2 wait limit, 4-7 w C, 8-15 X, 16-23 P and out
 constexpr uint32_t TILE = 32768;  // 128 rows x 128 bf16: [d 0-63 | d 64-127], 128-byte rows, swizzled
 
 // ---- instruction descriptors ----
@@ -39,8 +42,8 @@ constexpr uint32_t IDESC_KM = idesc_bf16(128, 128, 0, 1);  // (wC)^T B, P C: B o
 
 struct Weights {        // fp32 tables in shared memory
   float pw[CH + 4];     // lam^i
+  float pwi[CH];        // s_intra lam^i
   float wfull[CH], wtail[CH];  // w_t of a full chunk and of the segment's last one
-  float cf[32];         // column factors of a 32-wide block of P
 };
 
 __device__ __forceinline__ void fill_weights(const Scan &p, Weights *w, float gh, int tail, int tid) {
@@ -50,51 +53,126 @@ __device__ __forceinline__ void fill_weights(const Scan &p, Weights *w, float gh
     w->wfull[tid] = p.s_upd * expf(gh * (float)rf);
     w->wtail[tid] = tid < tail ? p.s_upd * expf(gh * (float)rt) : 0.f;
   }
-  if (tid < 32) w->cf[tid] = expf(gh * (float)(p.back ? tid : 31 - tid));
+  if (tid < CH) w->pwi[tid] = p.s_intra * expf(gh * (float)tid);
 }
 
-// Rows [len, 128) of a tile <- 0, by the 512 epilogue threads: what TMA read there
-// belongs to the next sequence, and 0 * NaN would carry it over.
-__device__ __forceinline__ void zero_tail(unsigned char *tile, int len, int etid) {
-  for (int x = etid; x < (CH - len) * 16; x += 512) {
+// Rows [len, 128) of a tile <- 0, by `n` threads: what TMA read there belongs to the
+// next sequence, and 0 * NaN would carry it over.
+__device__ __forceinline__ void zero_tail(unsigned char *tile, int len, int thread, int n) {
+  for (int x = thread; x < (CH - len) * 16; x += n) {
     const int r = len + (x >> 4), ch = x & 15;
     *reinterpret_cast<uint4 *>(tile + (ch >> 3) * 16384 + r * 128 + (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
-// (w C)^T as the A operand of dX: lane = row of X (column `row` of C), token pairs
-// [32 q, 32 q + 32) in three bf16 terms of 16 words each.
-__device__ __forceinline__ void scale_split(const unsigned char *tile, const float *wt, int row, int q,
-                                            uint32_t t_hi, uint32_t t_mid, uint32_t t_lo) {
-  const unsigned char *base = tile + (row >> 6) * 16384 + 32 * q * 128 + (row & 7) * 2;
-  const uint32_t ch = (row & 63) >> 3;
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    uint32_t hi[8], mid[8], lo[8];
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      const float4 w4 = *reinterpret_cast<const float4 *>(wt + 32 * q + 16 * half + 2 * i);
-      const float w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int t = 16 * half + 2 * (i + k);
-        const uint32_t c0 = *reinterpret_cast<const unsigned short *>(base + t * 128 + ((ch ^ (t & 7)) << 4));
-        const uint32_t c1 =
-            *reinterpret_cast<const unsigned short *>(base + (t + 1) * 128 + ((ch ^ ((t + 1) & 7)) << 4));
-        float x0 = w[2 * k] * __uint_as_float(c0 << 16), x1 = w[2 * k + 1] * __uint_as_float(c1 << 16);
-        hi[i + k] = pack_bf16x2(x0, x1);
-        x0 -= __uint_as_float(hi[i + k] << 16);
-        x1 -= __uint_as_float(hi[i + k] & 0xffff0000u);
-        mid[i + k] = pack_bf16x2(x0, x1);
-        x0 -= __uint_as_float(mid[i + k] << 16);
-        x1 -= __uint_as_float(mid[i + k] & 0xffff0000u);
-        lo[i + k] = pack_bf16x2(x0, x1);
-      }
+// The kernels here run five roles at once on each SM sub-core, so their code is kept
+// short (few loops unrolled, a small wait): with everything unrolled the roles did not
+// fit the instruction caches together and ran at about five cycles an instruction.
+//
+// All lanes of a warp wait for a phase, for at most the limit in ctl[CTL_LIMIT] (in
+// 1024 clock cycles) and only while no role has given up.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *ctl, int32_t *status) {
+  bool ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+  if (!ok) {
+    const long long t0 = clock64();
+    bool over;
+    do {
+      ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+      over = __any_sync(0xffffffffu, ctl[CTL_ABORT] != 0 || ((clock64() - t0) >> 10) > ctl[CTL_LIMIT]);
+    } while (!ok && !over);
+    if (!ok) {
+      ctl[CTL_ABORT] = 1;
+      if ((threadIdx.x & 31) == 0) report_status(status, GDN_ERR_DEVICE_TIMEOUT);
+      return false;
     }
-    tmem_st8(t_hi + 16 * q + 8 * half, hi);
-    tmem_st8(t_mid + 16 * q + 8 * half, mid);
-    tmem_st8(t_lo + 16 * q + 8 * half, lo);
   }
+  tc_fence_after();
+  return true;
+}
+// The same for one thread, which then acts alone (the TMA producer).
+__device__ __forceinline__ bool wait_phase_alone(uint32_t bar, uint32_t parity, volatile int *ctl) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity))
+    if (ctl[CTL_ABORT] != 0 || ((clock64() - t0) >> 10) > ctl[CTL_LIMIT]) return false;
+  return true;
+}
+// The limit of a workspace header in units of 1024 cycles: microseconds at 2 GHz (the
+// clock is at most that), 2 s by default.
+__device__ __forceinline__ int wait_limit(const int32_t *status) {
+  const uint32_t us = header_wait_limit_us(status);
+  return us ? (int)(2u * min(us, 0x3fffffffu)) : 4000000;
+}
+
+// One 16-bit term of two fp32 values: their upper halves in one word, and what they
+// leave.  Three such terms hold all 24 bits of a value.
+__device__ __forceinline__ uint32_t cut_term(float &x0, float &x1) {
+  const uint32_t u0 = __float_as_uint(x0), u1 = __float_as_uint(x1);
+  x0 -= __uint_as_float(u0 & 0xffff0000u);
+  x1 -= __uint_as_float(u1 & 0xffff0000u);
+  return __byte_perm(u0, u1, 0x7632);
+}
+
+// Four 8 x 8 blocks of 16-bit values, transposed: word of lane l in block m = rows
+// 2 (l mod 4), + 1 of column l / 4.
+__device__ __forceinline__ void ldmatrix_x4_t(uint32_t addr, uint32_t *r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// 16 lanes x 8 columns: lane l holds row l / 4 (+ 8: odd words), column l mod 4 (+ 4:
+// words 2, 3).
+__device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
+// (w C)^T as the A operand of dX: 32 rows of X (columns 32 lq .. of C) by the tokens
+// [t0, t0 + 16 TT), a pair of tokens in a word, in NT bf16 terms at `hi`, `mid`, `lo`
+// (lane 32 lq of TMEM, 8 columns for 16 tokens).  C is read by transposing 8 x 8
+// blocks, whose lane layout is that of the 16-lane TMEM stores.
+template <int NT, int TT>
+__device__ __forceinline__ void scale_split(uint32_t tile, const float *wt, int lq, int lane, int t0, uint32_t hi,
+                                            uint32_t mid, uint32_t lo) {
+  // block m of a load: tokens 8 (m / 2) .., columns 8 (m mod 2) ..
+  const int tr = t0 + 8 * (lane >> 4) + (lane & 7);
+  const uint32_t base = tile + (lq >> 1) * 16384 + tr * 128;
+  const uint32_t ch = 4 * (lq & 1) + ((lane >> 3) & 1);
+  const float *wl = wt + t0 + 2 * (lane & 3);
+#pragma unroll 1
+  for (int i = 0; i < TT; ++i) {
+    const float2 w0 = *reinterpret_cast<const float2 *>(wl + 16 * i);
+    const float2 w1 = *reinterpret_cast<const float2 *>(wl + 16 * i + 8);
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      uint32_t r[4], h[4], m[4], l[4];
+      ldmatrix_x4_t(base + i * 2048 + (((ch + 2 * d) ^ (tr & 7)) << 4), r);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 wk = k < 2 ? w0 : w1;
+        float x0 = wk.x * __uint_as_float(r[k] << 16), x1 = wk.y * __uint_as_float(r[k] & 0xffff0000u);
+        h[k] = cut_term(x0, x1);
+        m[k] = cut_term(x0, x1);
+        if (NT == 3) l[k] = cut_term(x0, x1);
+      }
+      const uint32_t at = ((uint32_t)(16 * d) << 16) + 8 * i;
+      tmem_st_16x8(hi + at, h);
+      tmem_st_16x8(mid + at, m);
+      if (NT == 3) tmem_st_16x8(lo + at, l);
+    }
+  }
+}
+
+// Registers of a thread, set by each warpgroup: a CTA is launched with 768 x 80, and
+// 128 x 40 + 128 x 56 + 256 x 104 + 256 x 88 is the same sum.
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 __device__ __forceinline__ void st_global_32b(void *p, const uint32_t *w) {
@@ -109,24 +187,31 @@ constexpr uint32_t STAGE = 3 * TILE;
 constexpr uint32_t OFF_X = 2 * STAGE;
 constexpr uint32_t OFF_W = OFF_X + TILE;
 constexpr uint32_t OFF_BAR = OFF_W + ((sizeof(Weights) + 15) / 16) * 16;
-constexpr uint32_t OFF_CTL = OFF_BAR + 128;  // TMEM base, control words
+constexpr uint32_t OFF_CTL = OFF_BAR + 160;  // TMEM base, control words
 constexpr uint32_t SMEM_OUT = OFF_CTL + 32;
 static_assert(SMEM_OUT <= 232448, "shared memory of a CTA");
 
-// TMEM columns.  P (fp32) is overwritten by its own bf16 form, and the columns that
-// frees take the low terms of w C; the others share the columns of Oa, which dX, issued
-// before, has finished reading when Oa is written.
-constexpr uint32_t R_P = 0, T_PB = 0, T_VL = 64, R_OI = 128, R_OA = 256, T_VH = 256, T_VM = 320, R_DX = 384;
+// TMEM columns: P (fp32), whose two halves are overwritten by their bf16 form and the
+// low terms of w C (32 columns each); O; the high and middle terms of w C; dX.  (MMAs
+// of one issuer run in order, so P may be written where the product before read.)
+constexpr uint32_t R_P = 0, T_PB = 0, T_VL = 32, R_O = 128, T_VH = 256, T_VM = 320, R_DX = 384;
+__host__ __device__ constexpr uint32_t pcol(int kk) { return 64 * (kk >> 2) + 8 * (kk & 3); }  // of T_PB, T_VL
 
-enum { B_FULL = 0, B_EMPTY = 2, B_P = 4, B_PREAD = 5, B_PB = 9, B_V = 10, B_DX = 11, B_OA = 12, B_X = 13, B_FIX = 14,
-       B_DRAIN = 15, NBAR = 16 };
-static_assert(NBAR * 8 <= 128, "barrier area");
+enum { B_FULL = 0, B_EMPTY = 2, B_P = 4, B_PREAD = 5, B_PB = 6, B_V = 7, B_VFREE = 9, B_DX = 11, B_DXFREE = 12, B_OI = 13,
+       B_OA = 14, B_OFREE = 15, B_X = 16, B_FIX = 17, B_DRAIN = 18, NBAR = 20 };
+static_assert(NBAR * 8 <= 160, "barrier area");
 
-// One CTA per (segment, head).  The 16 epilogue warps go through a chunk's four
-// elementwise phases together (P, w C, X, out), 32 elements a thread each, while the
-// tensor pipe works on the products already fed.
-template <typename TO>
-__global__ void __launch_bounds__(NTHREADS, 1)
+// One CTA per (segment, head).  Only X <- lam^len X + dX is carried from chunk to
+// chunk; dX, P and the rest of a chunk do not wait for the one before, except for the
+// buffers.  So each kind of work has its own warps, which run as far ahead as the
+// buffers let them:
+//   warps 4-7    w C as bf16 terms, in two halves of 64 tokens with a buffer each
+//   warps 8-15   X: adds dX, writes X as an operand
+//   warps 16-23  P to its causal bf16 form; scales A X^T in place (the product with P
+//                then adds to it); stores the outputs
+//   warp 1 issues P, A X^T and the product with P; warp 3 issues dX.
+template <typename TO, bool BACK>
+__global__ void __launch_bounds__(NTHREADS_O, 1)
 scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                    const __grid_constant__ CUtensorMap tm_c, const Scan p) {
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -145,11 +230,14 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
   }
   if (tid == 0) {
     for (int i = 0; i < NBAR; ++i) {
-      const bool all = i == B_PB || i == B_V || i == B_X || i == B_FIX;  // every epilogue warp
-      mbar_init(bar(i), all ? 16 : (i >= B_PREAD && i < B_PREAD + 4) ? 4 : 1);
+      // one arrival per warp of the group that signals; a stage is freed by both issuers
+      const bool eight = i == B_PREAD || i == B_PB || i == B_DXFREE || i == B_OFREE || i == B_X;
+      const bool four = i == B_V || i == B_V + 1 || i == B_FIX;
+      const bool two = i == B_EMPTY || i == B_EMPTY + 1 || i == B_DRAIN;
+      mbar_init(bar(i), eight ? 8 : four ? 4 : two ? 2 : 1);
     }
     ctl[CTL_ABORT] = 0;
-    ctl[CTL_LIMIT] = 0;
+    ctl[CTL_LIMIT] = 4000000;  // until warp 2 has read the header
     fence_barrier_init();
   }
   const float gh = head_decay(p, u.h);
@@ -162,28 +250,35 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + OFF_CTL);
-  // the chunk of a step, and whether it is the segment's short last one
-  auto chunk_of = [&](int ci) { return p.back ? nch - 1 - ci : ci; };
-  auto warp_wait = [&](int b, uint32_t parity) {
-    int ok = 1;
-    if (lane == 0 && !(ok = mbar_wait(bar(b), parity, ctl))) {
-      ctl[CTL_ABORT] = 1;
-      report_status(p.status, GDN_ERR_DEVICE_TIMEOUT);
-    }
-    ok = __shfl_sync(0xffffffffu, ok, 0);
+  const bool exact = u.last && p.xf;  // the state is returned: three terms
+  auto chunk_of = [&](int ci) { return BACK ? nch - 1 - ci : ci; };
+  auto arrive = [&](int b) {
     __syncwarp();
-    if (ok) tc_fence_after();
-    return ok != 0;
+    if (lane == 0) mbar_arrive(bar(b));
   };
+  auto warp_wait = [&](int b, uint32_t parity) { return wait_phase(bar(b), parity, ctl, p.status); };
 
+  if (warp < 4) fewer_registers<40>();
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       const int ha = u.h / (p.Hv / p.Ha), hb = u.h / (p.Hv / p.Hb), hc = u.h / (p.Hv / p.Hc);
       int issued = 0;
+      auto prefetch = [&](int ci) {  // into L2, two chunks before the stage is free
+        if (ci >= nch) return;
+        const int t = u.t0 + chunk_of(ci) * CH;
+        for (int half = 0; half < 2; ++half) {
+          tma_prefetch_3d(&tm_a, 64 * half, ha, t);
+          tma_prefetch_3d(&tm_b, 64 * half, hb, t);
+          tma_prefetch_3d(&tm_c, 64 * half, hc, t);
+        }
+      };
+      prefetch(2);
+      prefetch(3);
       for (int ci = 0; ci < nch; ++ci) {
         const int s = ci & 1, t = u.t0 + chunk_of(ci) * CH;
-        if (!mbar_wait(bar(B_EMPTY + s), ((ci >> 1) & 1) ^ 1, ctl)) break;
+        if (ci >= 2) prefetch(ci + 2);
+        if (!wait_phase_alone(bar(B_EMPTY + s), ((ci >> 1) & 1) ^ 1, ctl)) break;
         const uint32_t st = sb + s * STAGE, fb = bar(B_FULL + s);
         mbar_arrive_expect_tx(fb, STAGE);
         for (int half = 0; half < 2; ++half) {
@@ -202,18 +297,19 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         mbar_wait_landed(bar(B_FULL + (ci & 1)), (ci >> 1) & 1, 50000000ull);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
+    // ------------------------------------------------------------ MMA issuer of the outputs
     const uint64_t dA0 = sdesc_sw128(sb, 16, 1024), dB0 = sdesc_sw128(sb + TILE, 16, 1024);
-    const uint64_t dBm0 = sdesc_sw128(sb + TILE, 16384, 1024), dCm0 = sdesc_sw128(sb + 2 * TILE, 16384, 1024);
-    const uint64_t dX = sdesc_sw128(sb + OFF_X, 16, 1024);
+    const uint64_t dCm0 = sdesc_sw128(sb + 2 * TILE, 16384, 1024), dX = sdesc_sw128(sb + OFF_X, 16, 1024);
     for (int ci = 0; ci < nch; ++ci) {
       const int s = ci & 1;
       const uint32_t ph = ci & 1;
       const uint64_t so = (uint64_t)(s * (STAGE >> 4));
       if (!warp_wait(B_FULL + s, (ci >> 1) & 1)) break;
       if (chunk_of(ci) == nch - 1 && tail < CH && !warp_wait(B_FIX, 0)) break;
+      // (P goes where the low terms of the chunk before were)
+      if (exact && ci > 0 && !warp_wait(B_DX, (ci - 1) & 1)) break;
       if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
         for (int ks = 0; ks < 8; ++ks) {
           const uint32_t k16 = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
           mma_bf16(tmem + R_P, dA0 + so + k16, dB0 + so + k16, IDESC_KK, ks > 0);
@@ -221,180 +317,244 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         mma_commit(bar(B_P));
       }
       __syncwarp();
-      if (!warp_wait(B_X, ph)) break;
+      if (!warp_wait(B_X, ph) || (ci > 0 && !warp_wait(B_OFREE, (ci - 1) & 1))) break;
       if (elect_one()) {
-#pragma unroll
+#pragma unroll 1
         for (int ks = 0; ks < 8; ++ks) {
           const uint32_t k16 = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
-          mma_bf16(tmem + R_OI, dA0 + so + k16, dX + k16, IDESC_KK, ks > 0);
+          mma_bf16(tmem + R_O, dA0 + so + k16, dX + k16, IDESC_KK, ks > 0);
         }
-      }
-      __syncwarp();
-      if (!warp_wait(B_V, ph)) break;
-      if (elect_one()) {
-#pragma unroll
-        for (int ks = 0; ks < 24; ++ks) {  // low terms first
-          const int kk = ks & 7;
-          const uint32_t ta = ks < 8 ? T_VL : ks < 16 ? T_VM : T_VH;
-          mma_bf16_ts(tmem + R_DX, tmem + ta + 8 * kk, dBm0 + so + ((kk * 2048) >> 4), IDESC_KM, ks > 0);
-        }
-        mma_commit(bar(B_DX));
+        mma_commit(bar(B_OI));
       }
       __syncwarp();
       if (!warp_wait(B_PB, ph)) break;
       if (elect_one()) {
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_bf16_ts(tmem + R_OA, tmem + T_PB + 8 * ks, dCm0 + so + ((ks * 2048) >> 4), IDESC_KM, ks > 0);
+#pragma unroll 1
+        for (int kk = 0; kk < 8; ++kk)
+          mma_bf16_ts(tmem + R_O, tmem + T_PB + pcol(kk), dCm0 + so + ((kk * 2048) >> 4), IDESC_KM, 1);
         mma_commit(bar(B_OA));
         mma_commit(bar(B_EMPTY + s));
       }
       __syncwarp();
     }
-    // Drain: every MMA this warp issued finishes before TMEM is freed.
+    if (elect_one()) mma_commit(bar(B_DRAIN));
+    __syncwarp();
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ MMA issuer of dX
+    const uint64_t dBm0 = sdesc_sw128(sb + TILE, 16384, 1024);
+    for (int ci = 0; ci < nch; ++ci) {
+      const int s = ci & 1;
+      const uint32_t ph = ci & 1;
+      const uint64_t so = (uint64_t)(s * (STAGE >> 4));
+      if (!warp_wait(B_FULL + s, (ci >> 1) & 1)) break;
+      if (ci > 0 && !warp_wait(B_DXFREE, (ci - 1) & 1)) break;
+      bool ok = true;
+#pragma unroll 1
+      for (int hf = 0; hf < 2; ++hf) {
+        // (the terms are written after a short tile was zeroed)
+        if (!(ok = warp_wait(B_V + hf, ph))) break;
+        if (elect_one()) {
+#pragma unroll 1
+          for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk) {
+            const uint64_t db = dBm0 + so + ((kk * 2048) >> 4);
+            if (exact) mma_bf16_ts(tmem + R_DX, tmem + T_VL + pcol(kk), db, IDESC_KM, kk > 0);
+            mma_bf16_ts(tmem + R_DX, tmem + T_VM + 8 * kk, db, IDESC_KM, kk > 0 || exact);
+            mma_bf16_ts(tmem + R_DX, tmem + T_VH + 8 * kk, db, IDESC_KM, 1);
+          }
+          mma_commit(bar(B_VFREE + hf));
+          if (hf == 1) {
+            mma_commit(bar(B_DX));
+            mma_commit(bar(B_EMPTY + s));
+          }
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+    }
+    // Drain: every MMA that the two issuers sent finishes before TMEM is freed.
     if (elect_one()) {
       mma_commit(bar(B_DRAIN));
       mbar_wait_landed(bar(B_DRAIN), 0, 50000000ull);
     }
     __syncwarp();
   } else if (warp == 2) {
-    if (lane == 0) ctl[CTL_LIMIT] = (int)header_wait_limit_us(p.status);
-  } else if (warp >= 4) {
-    // ------------------------------------------------------------ epilogue
-    const int etid = tid - 128, q = etid >> 7;  // column quarter
-    const int lq = warp & 3, row = 32 * lq + lane;  // TMEM lane: token of P, Oi, Oa; row of X and dX
+    if (lane == 0) ctl[CTL_LIMIT] = wait_limit(p.status);
+  } else if (warp >= 4 && warp < 8) {
+    // ------------------------------------------------------------ w C
+    fewer_registers<56>();
+    const int gt = tid - 128, lq = warp & 3;
     const uint32_t tl = tmem + ((uint32_t)(32 * lq) << 16);
-    float X[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) X[i] = start_state(p, u, row, 32 * q + i);
+    for (int ci = 0; ci < nch; ++ci) {
+      const int s = ci & 1;
+      const uint32_t ph = ci & 1;
+      const bool last = chunk_of(ci) == nch - 1;
+      if (!warp_wait(B_FULL + s, (ci >> 1) & 1)) break;
+      if (last && tail < CH) {
+        unsigned char *st = smem + s * STAGE;
+        zero_tail(st + TILE, tail, gt, 128);
+        zero_tail(st + 2 * TILE, tail, gt, 128);
+        fence_proxy_async_smem();
+        arrive(B_FIX);
+        if (!warp_wait(B_FIX, 0)) break;  // rows that other warps have zeroed are read
+      }
+      const float *wt = last ? wts->wtail : wts->wfull;
+      const uint32_t ct = sb + s * STAGE + 2 * TILE;
+      if (exact && !warp_wait(B_PREAD, ph)) break;  // the low terms go where P was
+      bool ok = true;
+#pragma unroll 1
+      for (int hf = 0; hf < 2; ++hf) {
+        if (ci > 0 && !(ok = warp_wait(B_VFREE + hf, ph ^ 1))) break;
+        const uint32_t hi = tl + T_VH + 32 * hf, mid = tl + T_VM + 32 * hf, lo = tl + T_VL + 64 * hf;
+        if (exact) scale_split<3, 4>(ct, wt, lq, lane, 64 * hf, hi, mid, lo);
+        else scale_split<2, 4>(ct, wt, lq, lane, 64 * hf, hi, mid, 0);
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(B_V + hf);
+      }
+      if (!ok) break;
+    }
+  } else if (warp >= 8 && warp < 16) {
+    // ------------------------------------------------------------ X
+    more_registers<104>();
+    const int hf = (warp - 8) >> 2;                 // half of the columns of X
+    const int lq = warp & 3, row = 32 * lq + lane;  // TMEM lane: row of X and dX
+    const uint32_t tl = tmem + ((uint32_t)(32 * lq) << 16);
+    float X[64];
+    load_start<64>(p, u, gh, row, 64 * hf, X);
     auto put_x = [&]() {
-      unsigned char *xo = smem + OFF_X + (q >> 1) * 16384;
+      unsigned char *xo = smem + OFF_X + hf * 16384;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 8; ++c) {
         const float *x = X + 8 * c;
-        *reinterpret_cast<uint4 *>(xo + sw128_off(row, 4 * (q & 1) + c)) =
+        *reinterpret_cast<uint4 *>(xo + sw128_off(row, c)) =
             make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                        pack_bf16x2(x[6], x[7]));
       }
       fence_proxy_async_smem();
-    };
-    auto arrive = [&](int b) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(b));
-    };
-    if (nch > 0) {
-      put_x();
       arrive(B_X);
-    }
+    };
+    if (nch > 0) put_x();
     bool ok = true;
     for (int ci = 0; ci < nch; ++ci) {
-      const int s = ci & 1, c = chunk_of(ci);
       const uint32_t ph = ci & 1;
-      const bool last = c == nch - 1;
-      const int len = last ? tail : CH, skip = p.back && u.first && ci == 0 ? 1 : 0;
-      unsigned char *st = smem + s * STAGE;
-      if (!(ok = warp_wait(B_FULL + s, (ci >> 1) & 1))) break;
-      if (len < CH) {
-        zero_tail(st + TILE, len, etid);
-        zero_tail(st + 2 * TILE, len, etid);
-        fence_proxy_async_smem();
-        arrive(B_FIX);
-        // the w C phase reads rows that other warps have zeroed
-        if (!(ok = warp_wait(B_FIX, 0))) break;
-      }
-      // ---- P -> its causal, decayed part in bf16
-      if (!(ok = warp_wait(B_P, ph))) break;
-      uint32_t pb[16];
-      const bool off = p.back ? q > lq : q < lq;
-      if (off || q == lq) {
-        float v[32];
-        tmem_ld32(tl + R_P + 32 * q, v);
+      const int len = chunk_of(ci) == nch - 1 ? tail : CH, skip = BACK && u.first && ci == 0 ? 1 : 0;
+      if (!(ok = warp_wait(B_DX, ph))) break;
+      const float lx = wts->pw[len - skip];
+#pragma unroll
+      for (int i = 0; i < 64; i += 16) {
+        float d[16];
+        tmem_ld16(tl + R_DX + 64 * hf + i, d);
         tmem_wait_ld();
-        if (off) {
-          const float f = wts->pw[p.back ? 32 * q - row : row - 32 * q - 31];
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 c4 = *reinterpret_cast<const float4 *>(wts->cf + i);
-            pb[i / 2] = pack_bf16x2(v[i] * (f * c4.x), v[i + 1] * (f * c4.y));
-            pb[i / 2 + 1] = pack_bf16x2(v[i + 2] * (f * c4.z), v[i + 3] * (f * c4.w));
-          }
-        } else {
+        for (int k = 0; k < 16; ++k) X[i + k] = fmaf(lx, X[i + k], d[k]);
+      }
+      tc_fence_before();
+      arrive(B_DXFREE);
+      if (ci + 1 < nch) {
+        if (!(ok = warp_wait(B_OI, ph))) break;  // A X^T has read the operand
+        put_x();
+      }
+    }
+    if (ok && exact) {
+      const float f = BACK && nch > 0 ? expf(gh) : 1.f;
+      const size_t e0 = (((size_t)u.n * p.Hv + u.h) * HD + row) * HD + 64 * hf;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int d = p.back ? i - lane : lane - i;
-            v[i] = d >= 0 ? v[i] * wts->pw[d] : 0.f;
+      for (int i = 0; i < 64; i += 4) {
+        const float y[4] = {f * X[i], f * X[i + 1], f * X[i + 2], f * X[i + 3]};
+        store_state4(p.xf, e0 + i, p.x_bf16, y);
+      }
+    }
+  } else if (warp >= 16) {
+    // ------------------------------------------------------------ P and outputs
+    more_registers<88>();
+    const int hf = (warp - 16) >> 2;                // half of the columns of P and O
+    const int lq = warp & 3, row = 32 * lq + lane;  // TMEM lane: token
+    const uint32_t tl = tmem + ((uint32_t)(32 * lq) << 16);
+    const float lam = wts->pw[1];
+    for (int ci = 0; ci < nch; ++ci) {
+      const int c = chunk_of(ci);
+      const uint32_t ph = ci & 1;
+      const int len = c == nch - 1 ? tail : CH, skip = BACK && u.first && ci == 0 ? 1 : 0;
+      // ---- P -> its causal, decayed part in bf16
+      if (!warp_wait(B_P, ph)) break;
+#pragma unroll 1
+      for (int j = 0; j < 2; ++j) {
+        const int q = 2 * hf + j;  // 32-wide column block
+        uint32_t pb[16];
+        if (BACK ? q >= lq : q <= lq) {
+          float v[32];
+          tmem_ld32(tl + R_P + 32 * q, v);
+          tmem_wait_ld();
+          // times s_intra lam^{|t-s|}, from the nearest column of the block to the farthest
+          if (q != lq) {
+            float w = wts->pwi[BACK ? 32 * q - row : row - 32 * q - 31];
+#pragma unroll
+            for (int n = 0; n < 32; ++n) {
+              const int i = BACK ? n : 31 - n;
+              v[i] *= w;
+              w *= lam;
+            }
+          } else {
+            float w = 0.f;
+#pragma unroll
+            for (int n = 0; n < 32; ++n) {
+              const int i = BACK ? n : 31 - n;
+              if (i == lane) w = p.s_intra;
+              v[i] = (BACK ? i >= lane : i <= lane) ? v[i] * w : 0.f;
+              w *= lam;
+            }
           }
 #pragma unroll
           for (int i = 0; i < 16; ++i) pb[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-        }
-      } else {
+        } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) pb[i] = 0u;
+          for (int i = 0; i < 16; ++i) pb[i] = 0u;
+        }
+        // (over columns of P that this warp has read)
+        tmem_st16(tl + T_PB + 64 * hf + 16 * j, pb);
       }
-      // the columns of P are reused once the four warps of this lane quarter have read them
       tc_fence_before();
-      arrive(B_PREAD + lq);
-      if (!(ok = warp_wait(B_PREAD + lq, ph))) break;
-      tmem_st16(tl + T_PB + 16 * q, pb);
-      // ---- w C -> three bf16 terms
-      scale_split(st + 2 * TILE, last ? wts->wtail : wts->wfull, row, q, tl + T_VH, tl + T_VM, tl + T_VL);
+      arrive(B_PREAD);
+      // ---- A X^T, scaled in place
+      if (!warp_wait(B_OI, ph)) break;
+      const float wi = row < len ? p.s_inter * wts->pw[(BACK ? len - 1 - row : row) + 1 - skip] : 0.f;
+#pragma unroll 1
+      for (int i = 0; i < 64; i += 32) {
+        float v[32];
+        tmem_ld32(tl + R_O + 64 * hf + i, v);
+        tmem_wait_ld();
+        uint32_t w[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(wi * v[k]);
+        tmem_st32(tl + R_O + 64 * hf + i, w);
+      }
       tmem_wait_st();
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(B_V));
-        mbar_arrive(bar(B_PB));
-      }
-      // ---- X
-      if (!(ok = warp_wait(B_DX, ph))) break;
-      {
-        float d[32];
-        tmem_ld32(tl + R_DX + 32 * q, d);
+      arrive(B_PB);
+      // ---- outputs
+      if (!warp_wait(B_OA, ph)) break;
+      TO *o = static_cast<TO *>(p.out) + ((size_t)(u.t0 + c * CH + row) * p.Hv + u.h) * HD + 64 * hf;
+      constexpr int PER = 32 / sizeof(TO);  // elements of a 32-byte store
+#pragma unroll 1
+      for (int i = 0; i < 64; i += 32) {
+        float v[32];
+        tmem_ld32(tl + R_O + 64 * hf + i, v);
         tmem_wait_ld();
-        const float lx = wts->pw[len - skip];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) X[i] = fmaf(lx, X[i], d[i]);
-      }
-      if (ci + 1 < nch) put_x();
-      // ---- out
-      if (!(ok = warp_wait(B_OA, ph))) break;
-      {
-        float oi[32], oa[32];
-        tmem_ld32(tl + R_OI + 32 * q, oi);
-        tmem_ld32(tl + R_OA + 32 * q, oa);
-        tmem_wait_ld();
-        tc_fence_before();
-        arrive(B_X);
+        if (i == 32) {
+          tc_fence_before();
+          arrive(B_OFREE);
+        }
         if (row < len) {
-          const float wi = p.s_inter * wts->pw[(p.back ? len - 1 - row : row) + 1 - skip];
-          TO *o = static_cast<TO *>(p.out) + ((size_t)(u.t0 + c * CH + row) * p.Hv + u.h) * HD + 32 * q;
-          if (sizeof(TO) == 2) {
-            uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              w[i] = pack_bf16x2(fmaf(wi, oi[2 * i], p.s_intra * oa[2 * i]),
-                                 fmaf(wi, oi[2 * i + 1], p.s_intra * oa[2 * i + 1]));
-            st_global_32b(o, w);
-            st_global_32b(o + 16, w + 8);
-          } else {
+          for (int e = 0; e < 32; e += PER) {
+            uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint32_t w[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(fmaf(wi, oi[i + k], p.s_intra * oa[i + k]));
-              st_global_32b(o + i, w);
-            }
+            for (int k = 0; k < 8; ++k)
+              w[k] = sizeof(TO) == 2 ? pack_bf16x2(v[(e + 2 * k) % 32], v[(e + 2 * k + 1) % 32])
+                                     : __float_as_uint(v[e + k]);
+            st_global_32b(o + i + e, w);
           }
         }
-      }
-    }
-    if (ok && u.last && p.xf) {
-      const float f = p.back && nch > 0 ? expf(gh) : 1.f;
-      const size_t e0 = (((size_t)u.n * p.Hv + u.h) * HD + row) * HD + 32 * q;
-#pragma unroll
-      for (int i = 0; i < 32; i += 4) {
-        const float y[4] = {f * X[i], f * X[i + 1], f * X[i + 2], f * X[i + 3]};
-        store_state4(p.xf, e0 + i, p.x_bf16, y);
       }
     }
   }
@@ -441,7 +601,7 @@ scan_state_tc_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_cons
     for (int i = 0; i < S_NBAR; ++i)
       mbar_init(bar(i), i == S_V || i == S_V + 1 || i == S_FREE || i == S_FIX ? 16 : 1);
     ctl[CTL_ABORT] = 0;
-    ctl[CTL_LIMIT] = 0;
+    ctl[CTL_LIMIT] = 4000000;  // until warp 2 has read the header
     fence_barrier_init();
   }
   const float gh = head_decay(p, u.h);
@@ -455,17 +615,7 @@ scan_state_tc_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_cons
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + OFF_CTL_S);
   auto chunk_of = [&](int ci) { return p.back ? nch - 1 - ci : ci; };
-  auto warp_wait = [&](int b, uint32_t parity) {
-    int ok = 1;
-    if (lane == 0 && !(ok = mbar_wait(bar(b), parity, ctl))) {
-      ctl[CTL_ABORT] = 1;
-      report_status(p.status, GDN_ERR_DEVICE_TIMEOUT);
-    }
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    __syncwarp();
-    if (ok) tc_fence_after();
-    return ok != 0;
-  };
+  auto warp_wait = [&](int b, uint32_t parity) { return wait_phase(bar(b), parity, ctl, p.status); };
 
   if (warp == 0) {
     if (lane == 0) {
@@ -473,7 +623,7 @@ scan_state_tc_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_cons
       int issued = 0;
       for (int ci = 0; ci < nch; ++ci) {
         const int s = ci % NST_S, t = u.t0 + chunk_of(ci) * CH;
-        if (!mbar_wait(bar(S_EMPTY + s), ((ci / NST_S) & 1) ^ 1, ctl)) break;
+        if (!wait_phase_alone(bar(S_EMPTY + s), ((ci / NST_S) & 1) ^ 1, ctl)) break;
         const uint32_t st = sb + s * STAGE_S, fb = bar(S_FULL + s);
         mbar_arrive_expect_tx(fb, STAGE_S);
         for (int half = 0; half < 2; ++half) {
@@ -517,7 +667,7 @@ scan_state_tc_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_cons
     }
     __syncwarp();
   } else if (warp == 2) {
-    if (lane == 0) ctl[CTL_LIMIT] = (int)header_wait_limit_us(p.status);
+    if (lane == 0) ctl[CTL_LIMIT] = wait_limit(p.status);
   } else if (warp >= 4) {
     const int etid = tid - 128, q = etid >> 7, lq = warp & 3, row = 32 * lq + lane;
     const uint32_t tl = tmem + ((uint32_t)(32 * lq) << 16);
@@ -534,14 +684,15 @@ scan_state_tc_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_cons
       const bool last = chunk_of(ci) == nch - 1;
       if (!warp_wait(S_FULL + s, (ci / NST_S) & 1)) return false;
       if (last && tail < CH) {
-        zero_tail(st, tail, etid);
-        zero_tail(st + TILE, tail, etid);
+        zero_tail(st, tail, etid, 512);
+        zero_tail(st + TILE, tail, etid, 512);
         fence_proxy_async_smem();
         arrive(S_FIX);
         if (!warp_wait(S_FIX, 0)) return false;
       }
       const uint32_t tv = tl + S_TV + 192 * (ci & 1);
-      scale_split(st + TILE, last ? wts->wtail : wts->wfull, row, q, tv, tv + 64, tv + 128);
+      scale_split<3, 2>(sb + s * STAGE_S + TILE, last ? wts->wtail : wts->wfull, lq, lane, 32 * q, tv + 16 * q,
+                        tv + 64 + 16 * q, tv + 128 + 16 * q);
       tmem_wait_st();
       tc_fence_before();
       arrive(S_V + (ci & 1));
@@ -603,7 +754,7 @@ bool scan_tc_supported(const Scan &p, int dtype) {
 }
 
 cudaError_t launch_scan_tc(const Scan &p, int units, int out_dtype, cudaStream_t stream) {
-  static std::atomic<bool> f0[64], f1[64], f2[64];
+  static std::atomic<bool> f0[64], f1[64], f2[64], f3[64], f4[64];
   CUtensorMap ma, mb, mc;
   if (!make_map(&mb, p.b, p.Hb, p.T) || !make_map(&mc, p.c, p.Hc, p.T)) return cudaErrorInvalidValue;
   cudaError_t e;
@@ -616,11 +767,12 @@ cudaError_t launch_scan_tc(const Scan &p, int units, int out_dtype, cudaStream_t
   auto go = [&](auto kern, std::atomic<bool>(&flags)[64]) {
     const cudaError_t r = set_smem_once(kern, SMEM_OUT, flags);
     if (r != cudaSuccess) return r;
-    kern<<<(unsigned)units, NTHREADS, SMEM_OUT, stream>>>(ma, mb, mc, p);
+    kern<<<(unsigned)units, NTHREADS_O, SMEM_OUT, stream>>>(ma, mb, mc, p);
     return cudaGetLastError();
   };
-  if (out_dtype == GDN_DTYPE_BF16) return go(scan_out_tc_kernel<__nv_bfloat16>, f1);
-  return go(scan_out_tc_kernel<float>, f2);
+  if (out_dtype == GDN_DTYPE_BF16)
+    return p.back ? go(scan_out_tc_kernel<__nv_bfloat16, true>, f1) : go(scan_out_tc_kernel<__nv_bfloat16, false>, f2);
+  return p.back ? go(scan_out_tc_kernel<float, true>, f3) : go(scan_out_tc_kernel<float, false>, f4);
 }
 
 }  // namespace lin
