@@ -16,9 +16,9 @@
 // Sequences are cut into segments of L tokens.  (1) The state each segment adds
 // for the ones after it, all segments at once; (2) a prefix over the segments of each
 // sequence turns those into the state each segment starts from; (3) the outputs, all
-// segments at once, each walking its chunks from its start state, the last one of a
-// sequence writing the final state.  (1) and (2) only concern sequences longer than
-// L; where no sequence can be, (3) alone is launched.
+// segments at once, each walking its chunks from its start state.  The final state of
+// a sequence of several segments comes from (2), that of one from (3).  (1) and (2)
+// only concern sequences longer than L; where no sequence can be, (3) alone is launched.
 #pragma once
 
 #include <cuda.h>

@@ -91,7 +91,7 @@ struct Prefix {
   float *nat, *tr;
   int keep_nat;      // the starting states are wanted in nat
   const void *x0;    // [N, Hv, Dc, Da]
-  void *xf;          // final states: an empty sequence's is its initial one
+  void *xf;          // final states, of empty sequences and of several segments; NULL to skip
   int x_bf16;
 };
 
@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(256) prefix_kernel(const Prefix p) {
     const int sg = p.back ? cnt - 1 - i : i;
     const size_t at = ((size_t)(s0 + sg) * p.Hv + h) * state;
     float add[4];
-    if (i + 1 < cnt) load4(p.nat + at + in_state, add);  // before its place takes the starting state
+    const bool go_on = i + 1 < cnt || p.xf;
+    if (go_on) load4(p.nat + at + in_state, add);  // before its place takes the starting state
     if (p.keep_nat) *reinterpret_cast<float4 *>(p.nat + at + in_state) = make_float4(x[0], x[1], x[2], x[3]);
     if (p.tr) {
       __syncthreads();
@@ -126,11 +127,17 @@ __global__ void __launch_bounds__(256) prefix_kernel(const Prefix p) {
       *reinterpret_cast<float4 *>(p.tr + at + (size_t)(j0 + r) * p.Dc + i0 + c) =
           make_float4(tile[r][c], tile[r][c + 1], tile[r][c + 2], tile[r][c + 3]);
     }
-    if (i + 1 == cnt) break;
+    if (!go_on) break;
     const int tokens = min(p.L, len - sg * p.L) - (p.back && i == 0 ? 1 : 0);
     const float f = expf(gh * (float)tokens);
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[k] = fmaf(f, x[k], add[k]);
+  }
+  if (cnt > 1 && p.xf) {
+    const float f = p.back ? expf(gh) : 1.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] *= f;
+    store_state4(p.xf, e0, p.x_bf16, x);
   }
 }
 
@@ -178,7 +185,7 @@ __global__ void __launch_bounds__(256) scan_kernel(const Scan p) {
   const int unit = blockIdx.x / splits, dc0 = DCT * (blockIdx.x - unit * splits);
   Unit w;
   if (!get_unit(p, unit, w)) return;
-  if (!OUT && w.last) return;  // no segment starts from its end
+  if (!OUT && w.last && (w.first || !p.xf)) return;  // nothing starts from its end
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
   const int ha = w.h / (p.Hv / p.Ha), hb = w.h / (p.Hv / p.Hb), hc = w.h / (p.Hv / p.Hc);
   const float gh = head_decay(p, w.h);
@@ -316,7 +323,7 @@ __global__ void __launch_bounds__(256) scan_kernel(const Scan p) {
       put_x();
     }
   }
-  const bool fin = OUT && w.last && p.xf;
+  const bool fin = OUT && w.first && w.last && p.xf;
   if (OUT && !fin) return;
   const float f = fin && p.back && nch > 0 ? expf(gh) : 1.f;
   const size_t base = fin ? ((size_t)w.n * p.Hv + w.h) * p.Dc * p.Da
@@ -535,14 +542,13 @@ cudaError_t launch_linear_backward(const void *q, const void *k, const void *v, 
   p = base;  // D, for dv and dk
   p.back = 1;
   p.a = k; p.Ha = Hqk; p.b = q; p.Hb = Hqk; p.c = d_o; p.Hc = Hv; p.Da = Dk; p.Dc = Dv;
-  p.s_intra = p.s_upd = scale; p.s_inter = 1.f; p.seg_state = nat; p.x0 = dsf;
+  p.s_intra = p.s_upd = scale; p.s_inter = 1.f; p.seg_state = nat; p.x0 = dsf; p.xf = ds0;
   if (!one) {
     if ((e = run_scan(p, units, dtype, dtype, dtype, stream)) != cudaSuccess) return e;
     x.x0 = dsf; x.back = 1; x.keep_nat = 1; x.xf = ds0;
     if ((e = run_prefix(x, stream)) != cudaSuccess) return e;
   }
   p.out = dv;
-  p.xf = ds0;
   if ((e = run_scan(p, units, dtype, dtype, dtype, stream)) != cudaSuccess) return e;
   p.a = v; p.Ha = Hv; p.b = d_o; p.Hb = Hv; p.c = q; p.Hc = Hqk; p.Da = Dv; p.Dc = Dk;
   p.seg_state = tr; p.x0_tr = 1; p.xf = nullptr;

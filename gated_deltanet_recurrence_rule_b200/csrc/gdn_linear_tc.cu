@@ -33,7 +33,7 @@ namespace {
 
 constexpr int CH = 128, HD = 128;
 constexpr int NTHREADS = 640;   // states: warp 0 TMA, 1 MMA, 2 wait limit, 4-19 elementwise
-constexpr int NTHREADS_O = 768; // outputs: warp 0 TMA, 1 and 3 MMA, 2 wait limit, 4-7 w C, 8-15 X, 16-23 P and out
+constexpr int NTHREADS_O = 1024;  // outputs: warp 0 loads, 1 and 3 MMA, 2 stores, 4-7 w C, 8-15 X, 16-23 P, 24-31 out
 constexpr uint32_t TILE = 32768;  // 128 rows x 128 bf16: [d 0-63 | d 64-127], 128-byte rows, swizzled
 
 // ---- instruction descriptors ----
@@ -129,12 +129,13 @@ __device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, const uint32_t *r) 
 }
 
 // (w C)^T as the A operand of dX: 32 rows of X (columns 32 lq .. of C) by the tokens
-// [t0, t0 + 16 TT), a pair of tokens in a word, in NT bf16 terms at `hi`, `mid`, `lo`
-// (lane 32 lq of TMEM, 8 columns for 16 tokens).  C is read by transposing 8 x 8
-// blocks, whose lane layout is that of the 16-lane TMEM stores.
-template <int NT, int TT>
-__device__ __forceinline__ void scale_split(uint32_t tile, const float *wt, int lq, int lane, int t0, uint32_t hi,
-                                            uint32_t mid, uint32_t lo) {
+// [t0, t0 + 16 TT), a pair of tokens in a word, 8 columns for 16 tokens (lane 32 lq of
+// TMEM).  TERMS: 3, the high, middle and low terms at t1, t2, t3; 2, the first two;
+// 1, the low term alone at t1.  C is read by transposing 8 x 8 blocks, whose lane
+// layout is that of the 16-lane TMEM stores.
+template <int TERMS, int TT>
+__device__ __forceinline__ void scale_split(uint32_t tile, const float *wt, int lq, int lane, int t0, uint32_t t1,
+                                            uint32_t t2, uint32_t t3) {
   // block m of a load: tokens 8 (m / 2) .., columns 8 (m mod 2) ..
   const int tr = t0 + 8 * (lane >> 4) + (lane & 7);
   const uint32_t base = tile + (lq >> 1) * 16384 + tr * 128;
@@ -154,18 +155,21 @@ __device__ __forceinline__ void scale_split(uint32_t tile, const float *wt, int 
         float x0 = wk.x * __uint_as_float(r[k] << 16), x1 = wk.y * __uint_as_float(r[k] & 0xffff0000u);
         h[k] = cut_term(x0, x1);
         m[k] = cut_term(x0, x1);
-        if (NT == 3) l[k] = cut_term(x0, x1);
+        if (TERMS != 2) l[k] = cut_term(x0, x1);
       }
       const uint32_t at = ((uint32_t)(16 * d) << 16) + 8 * i;
-      tmem_st_16x8(hi + at, h);
-      tmem_st_16x8(mid + at, m);
-      if (NT == 3) tmem_st_16x8(lo + at, l);
+      if (TERMS > 1) {
+        tmem_st_16x8(t1 + at, h);
+        tmem_st_16x8(t2 + at, m);
+      }
+      if (TERMS == 3) tmem_st_16x8(t3 + at, l);
+      if (TERMS == 1) tmem_st_16x8(t1 + at, l);
     }
   }
 }
 
-// Registers of a thread, set by each warpgroup: a CTA is launched with 768 x 80, and
-// 128 x 40 + 128 x 56 + 256 x 104 + 256 x 88 is the same sum.
+// Registers of a thread, set by each warpgroup: a CTA is launched with 1024 x 64, and
+// 128 x 32 + 128 x 48 + 256 x 104 + 256 x 64 + 256 x 48 is the same sum.
 template <int N>
 __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -175,45 +179,43 @@ __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-__device__ __forceinline__ void st_global_32b(void *p, const uint32_t *w) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-
 // ---------------------------------------------------------------- outputs
 // Shared memory of the output kernel: 2 stages of A, B, C tiles, X as an operand.
 constexpr uint32_t STAGE = 3 * TILE;
 constexpr uint32_t OFF_X = 2 * STAGE;
 constexpr uint32_t OFF_W = OFF_X + TILE;
 constexpr uint32_t OFF_BAR = OFF_W + ((sizeof(Weights) + 15) / 16) * 16;
-constexpr uint32_t OFF_CTL = OFF_BAR + 160;  // TMEM base, control words
+constexpr uint32_t OFF_CTL = OFF_BAR + 192;  // TMEM base, control words
 constexpr uint32_t SMEM_OUT = OFF_CTL + 32;
 static_assert(SMEM_OUT <= 232448, "shared memory of a CTA");
 
-// TMEM columns: P (fp32), whose two halves are overwritten by their bf16 form and the
-// low terms of w C (32 columns each); O; the high and middle terms of w C; dX.  (MMAs
-// of one issuer run in order, so P may be written where the product before read.)
-constexpr uint32_t R_P = 0, T_PB = 0, T_VL = 32, R_O = 128, T_VH = 256, T_VM = 320, R_DX = 384;
-__host__ __device__ constexpr uint32_t pcol(int kk) { return 64 * (kk >> 2) + 8 * (kk & 3); }  // of T_PB, T_VL
+// TMEM columns: P (fp32), whose two halves are overwritten by their bf16 form (32
+// columns each); O; two terms of w C; dX.  (MMAs of one issuer run in order, so P may
+// be written where the product before read.)
+constexpr uint32_t R_P = 0, T_PB = 0, R_O = 128, T_VH = 256, T_VM = 320, R_DX = 384;
+__host__ __device__ constexpr uint32_t pcol(int kk) { return 64 * (kk >> 2) + 8 * (kk & 3); }  // of T_PB
 
-enum { B_FULL = 0, B_EMPTY = 2, B_P = 4, B_PREAD = 5, B_PB = 6, B_V = 7, B_VFREE = 9, B_DX = 11, B_DXFREE = 12, B_OI = 13,
-       B_OA = 14, B_OFREE = 15, B_X = 16, B_FIX = 17, B_DRAIN = 18, NBAR = 20 };
-static_assert(NBAR * 8 <= 160, "barrier area");
+enum { B_FULL = 0, B_EMPTY = 2, B_P = 4, B_PB = 6, B_V = 7, B_VFREE = 9, B_DX = 11, B_DXFREE = 12, B_OI = 13,
+       B_OA = 14, B_OFREE = 15, B_X = 16, B_FIX = 17, B_DRAIN = 18, B_EMPTYA = 19, B_OUT = 21, B_OUTFREE = 22, NBAR = 23 };
+static_assert(NBAR * 8 <= 192, "barrier area");
 
 // One CTA per (segment, head).  Only X <- lam^len X + dX is carried from chunk to
 // chunk; dX, P and the rest of a chunk do not wait for the one before, except for the
 // buffers.  So each kind of work has its own warps, which run as far ahead as the
 // buffers let them:
-//   warps 4-7    w C as bf16 terms, in two halves of 64 tokens with a buffer each
+//   warps 4-7    w C as bf16 terms, in two halves of 64 tokens with a buffer each; a
+//                third term goes into the first one's buffer when that has been used
 //   warps 8-15   X: adds dX, writes X as an operand
-//   warps 16-23  P to its causal bf16 form; scales A X^T in place (the product with P
-//                then adds to it); stores the outputs
-//   warp 1 issues P, A X^T and the product with P; warp 3 issues dX.
+//   warps 16-23  P to its causal bf16 form
+//   warps 24-31  scale A X^T in place (the product with P then adds to it), and put the
+//                outputs where the chunk's A tile was
+//   warp 2 stores them from there by TMA (a direct store of 32 rows by a warp is 32
+//   scattered pieces, about 85 cycles of the load-store unit); warp 1 issues P, A X^T
+//   and the product with P; warp 3 issues dX.
 template <typename TO, bool BACK>
 __global__ void __launch_bounds__(NTHREADS_O, 1)
 scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                   const __grid_constant__ CUtensorMap tm_c, const Scan p) {
+                   const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_o, const Scan p) {
   extern __shared__ __align__(1024) unsigned char smem[];
   Unit u;
   if (!get_unit(p, blockIdx.x, u)) return;
@@ -231,10 +233,10 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
   if (tid == 0) {
     for (int i = 0; i < NBAR; ++i) {
       // one arrival per warp of the group that signals; a stage is freed by both issuers
-      const bool eight = i == B_PREAD || i == B_PB || i == B_DXFREE || i == B_OFREE || i == B_X;
+      const bool eight = i == B_DXFREE || i == B_OFREE || i == B_X || i == B_OUT;
       const bool four = i == B_V || i == B_V + 1 || i == B_FIX;
       const bool two = i == B_EMPTY || i == B_EMPTY + 1 || i == B_DRAIN;
-      mbar_init(bar(i), eight ? 8 : four ? 4 : two ? 2 : 1);
+      mbar_init(bar(i), i == B_PB ? 16 : eight ? 8 : four ? 4 : two ? 2 : 1);
     }
     ctl[CTL_ABORT] = 0;
     ctl[CTL_LIMIT] = 4000000;  // until warp 2 has read the header
@@ -250,7 +252,8 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + OFF_CTL);
-  const bool exact = u.last && p.xf;  // the state is returned: three terms
+  const bool exact = u.first && u.last && p.xf;  // the state is returned: three terms
+  const int parts = exact ? 4 : 2;               // of dX
   auto chunk_of = [&](int ci) { return BACK ? nch - 1 - ci : ci; };
   auto arrive = [&](int b) {
     __syncwarp();
@@ -258,7 +261,7 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
   };
   auto warp_wait = [&](int b, uint32_t parity) { return wait_phase(bar(b), parity, ctl, p.status); };
 
-  if (warp < 4) fewer_registers<40>();
+  if (warp < 4) fewer_registers<32>();
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
@@ -282,13 +285,16 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         const uint32_t st = sb + s * STAGE, fb = bar(B_FULL + s);
         mbar_arrive_expect_tx(fb, STAGE);
         for (int half = 0; half < 2; ++half) {
-          tma_load_3d(st + half * 16384, &tm_a, fb, 64 * half, ha, t);
           tma_load_3d(st + TILE + half * 16384, &tm_b, fb, 64 * half, hb, t);
           tma_load_3d(st + 2 * TILE + half * 16384, &tm_c, fb, 64 * half, hc, t);
         }
+        // the outputs have left the place of A
+        const bool a_free = wait_phase_alone(bar(B_EMPTYA + s), ((ci >> 1) & 1) ^ 1, ctl);
+        for (int half = 0; half < 2; ++half) tma_load_3d(st + half * 16384, &tm_a, fb, 64 * half, ha, t);
         issued = ci + 1;
+        if (!a_free) break;
       }
-      if (issued < nch) {
+      if (issued < nch || ctl[CTL_ABORT]) {
         ctl[CTL_ABORT] = 1;
         report_status(p.status, GDN_ERR_DEVICE_TIMEOUT);
       }
@@ -306,8 +312,6 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
       const uint64_t so = (uint64_t)(s * (STAGE >> 4));
       if (!warp_wait(B_FULL + s, (ci >> 1) & 1)) break;
       if (chunk_of(ci) == nch - 1 && tail < CH && !warp_wait(B_FIX, 0)) break;
-      // (P goes where the low terms of the chunk before were)
-      if (exact && ci > 0 && !warp_wait(B_DX, (ci - 1) & 1)) break;
       if (elect_one()) {
 #pragma unroll 1
         for (int ks = 0; ks < 8; ++ks) {
@@ -350,19 +354,19 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
       if (ci > 0 && !warp_wait(B_DXFREE, (ci - 1) & 1)) break;
       bool ok = true;
 #pragma unroll 1
-      for (int hf = 0; hf < 2; ++hf) {
+      for (int j = 0; j < parts; ++j) {  // halves of the tokens; again for the third term
+        const int hf = j & 1;
         // (the terms are written after a short tile was zeroed)
-        if (!(ok = warp_wait(B_V + hf, ph))) break;
+        if (!(ok = warp_wait(B_V + hf, (parts / 2 * ci + (j >> 1)) & 1))) break;
         if (elect_one()) {
 #pragma unroll 1
           for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk) {
             const uint64_t db = dBm0 + so + ((kk * 2048) >> 4);
-            if (exact) mma_bf16_ts(tmem + R_DX, tmem + T_VL + pcol(kk), db, IDESC_KM, kk > 0);
-            mma_bf16_ts(tmem + R_DX, tmem + T_VM + 8 * kk, db, IDESC_KM, kk > 0 || exact);
-            mma_bf16_ts(tmem + R_DX, tmem + T_VH + 8 * kk, db, IDESC_KM, 1);
+            mma_bf16_ts(tmem + R_DX, tmem + T_VH + 8 * kk, db, IDESC_KM, j + kk > 0);
+            if (j < 2) mma_bf16_ts(tmem + R_DX, tmem + T_VM + 8 * kk, db, IDESC_KM, 1);
           }
           mma_commit(bar(B_VFREE + hf));
-          if (hf == 1) {
+          if (j == parts - 1) {
             mma_commit(bar(B_DX));
             mma_commit(bar(B_EMPTY + s));
           }
@@ -378,15 +382,39 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     }
     __syncwarp();
   } else if (warp == 2) {
+    // ------------------------------------------------------------ stores
     if (lane == 0) ctl[CTL_LIMIT] = wait_limit(p.status);
+    __syncwarp();
+    constexpr int BOXES = sizeof(TO) / 2;  // of 128 bytes a row, for 64 columns
+    for (int ci = 0; ci < nch; ++ci) {
+      const int c = chunk_of(ci), s = ci & 1;
+      const int len = c == nch - 1 ? tail : CH;
+#pragma unroll 1
+      for (int j = 0; j < BOXES; ++j) {
+        if (!warp_wait(B_OUT, (BOXES * ci + j) & 1)) break;
+        if (lane == 0) {
+          // boxes of 32 rows that end inside the sequence
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            const int hf = i >> 2, r = 32 * (i & 3);
+            if (r + 32 <= len)
+              tma_store_3d(&tm_o, sb + s * STAGE + hf * 16384 + r * 128, 64 * hf + j * 32, u.h, u.t0 + c * CH + r);
+          }
+          bulk_commit_group();
+          bulk_wait_read_all();
+          mbar_arrive(bar(j + 1 < BOXES ? B_OUTFREE : B_EMPTYA + s));
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) bulk_wait_all();
   } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------ w C
-    fewer_registers<56>();
+    fewer_registers<48>();
     const int gt = tid - 128, lq = warp & 3;
     const uint32_t tl = tmem + ((uint32_t)(32 * lq) << 16);
     for (int ci = 0; ci < nch; ++ci) {
       const int s = ci & 1;
-      const uint32_t ph = ci & 1;
       const bool last = chunk_of(ci) == nch - 1;
       if (!warp_wait(B_FULL + s, (ci >> 1) & 1)) break;
       if (last && tail < CH) {
@@ -399,14 +427,14 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
       }
       const float *wt = last ? wts->wtail : wts->wfull;
       const uint32_t ct = sb + s * STAGE + 2 * TILE;
-      if (exact && !warp_wait(B_PREAD, ph)) break;  // the low terms go where P was
       bool ok = true;
 #pragma unroll 1
-      for (int hf = 0; hf < 2; ++hf) {
-        if (ci > 0 && !(ok = warp_wait(B_VFREE + hf, ph ^ 1))) break;
-        const uint32_t hi = tl + T_VH + 32 * hf, mid = tl + T_VM + 32 * hf, lo = tl + T_VL + 64 * hf;
-        if (exact) scale_split<3, 4>(ct, wt, lq, lane, 64 * hf, hi, mid, lo);
-        else scale_split<2, 4>(ct, wt, lq, lane, 64 * hf, hi, mid, 0);
+      for (int j = 0; j < parts; ++j) {
+        const int hf = j & 1, n = parts / 2 * ci + (j >> 1);  // n: uses of the buffer before
+        if (n > 0 && !(ok = warp_wait(B_VFREE + hf, (n - 1) & 1))) break;
+        const uint32_t hi = tl + T_VH + 32 * hf, mid = tl + T_VM + 32 * hf;
+        if (j < 2) scale_split<2, 4>(ct, wt, lq, lane, 64 * hf, hi, mid, 0);
+        else scale_split<1, 4>(ct, wt, lq, lane, 64 * hf, hi, 0, 0);
         tmem_wait_st();
         tc_fence_before();
         arrive(B_V + hf);
@@ -464,23 +492,19 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         store_state4(p.xf, e0 + i, p.x_bf16, y);
       }
     }
-  } else if (warp >= 16) {
-    // ------------------------------------------------------------ P and outputs
-    more_registers<88>();
-    const int hf = (warp - 16) >> 2;                // half of the columns of P and O
+  } else if (warp >= 16 && warp < 24) {
+    // ------------------------------------------------------------ P -> its causal, decayed part in bf16
+    fewer_registers<64>();
+    const int hf = (warp - 16) >> 2;                // half of the columns of P
     const int lq = warp & 3, row = 32 * lq + lane;  // TMEM lane: token
     const uint32_t tl = tmem + ((uint32_t)(32 * lq) << 16);
     const float lam = wts->pw[1];
     for (int ci = 0; ci < nch; ++ci) {
-      const int c = chunk_of(ci);
-      const uint32_t ph = ci & 1;
-      const int len = c == nch - 1 ? tail : CH, skip = BACK && u.first && ci == 0 ? 1 : 0;
-      // ---- P -> its causal, decayed part in bf16
-      if (!warp_wait(B_P, ph)) break;
+      if (!warp_wait(B_P, ci & 1)) break;
+      uint32_t pb[16];
 #pragma unroll 1
       for (int j = 0; j < 2; ++j) {
         const int q = 2 * hf + j;  // 32-wide column block
-        uint32_t pb[16];
         if (BACK ? q >= lq : q <= lq) {
           float v[32];
           tmem_ld32(tl + R_P + 32 * q, v);
@@ -513,49 +537,75 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         // (over columns of P that this warp has read)
         tmem_st16(tl + T_PB + 64 * hf + 16 * j, pb);
       }
+      tmem_wait_st();
       tc_fence_before();
-      arrive(B_PREAD);
-      // ---- A X^T, scaled in place
+      arrive(B_PB);
+    }
+  } else if (warp >= 24) {
+    // ------------------------------------------------------------ A X^T scaled in place; outputs
+    fewer_registers<48>();
+    const int hf = (warp - 24) >> 2;                // half of the columns of O
+    const int lq = warp & 3, row = 32 * lq + lane;  // TMEM lane: token
+    const uint32_t tl = tmem + ((uint32_t)(32 * lq) << 16) + R_O + 64 * hf;
+    constexpr int COLS = 128 / sizeof(TO);          // columns of a 128-byte row of a store
+    for (int ci = 0; ci < nch; ++ci) {
+      const int c = chunk_of(ci), s = ci & 1;
+      const uint32_t ph = ci & 1;
+      const int len = c == nch - 1 ? tail : CH, skip = BACK && u.first && ci == 0 ? 1 : 0;
       if (!warp_wait(B_OI, ph)) break;
       const float wi = row < len ? p.s_inter * wts->pw[(BACK ? len - 1 - row : row) + 1 - skip] : 0.f;
 #pragma unroll 1
       for (int i = 0; i < 64; i += 32) {
         float v[32];
-        tmem_ld32(tl + R_O + 64 * hf + i, v);
+        tmem_ld32(tl + i, v);
         tmem_wait_ld();
         uint32_t w[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(wi * v[k]);
-        tmem_st32(tl + R_O + 64 * hf + i, w);
+        tmem_st32(tl + i, w);
       }
       tmem_wait_st();
       tc_fence_before();
       arrive(B_PB);
-      // ---- outputs
       if (!warp_wait(B_OA, ph)) break;
-      TO *o = static_cast<TO *>(p.out) + ((size_t)(u.t0 + c * CH + row) * p.Hv + u.h) * HD + 64 * hf;
-      constexpr int PER = 32 / sizeof(TO);  // elements of a 32-byte store
+      // rows of this warp: a 4096-byte box of 32 rows at its place in the A tile
+      unsigned char *box = smem + s * STAGE + hf * 16384 + lq * 4096;
+      const bool whole = 32 * lq + 32 <= len;
+      bool ok = true;
 #pragma unroll 1
-      for (int i = 0; i < 64; i += 32) {
-        float v[32];
-        tmem_ld32(tl + R_O + 64 * hf + i, v);
-        tmem_wait_ld();
-        if (i == 32) {
-          tc_fence_before();
-          arrive(B_OFREE);
-        }
-        if (row < len) {
+      for (int j = 0; j < 64; j += COLS) {
+        // (fp32: the second 32 columns take the place of the first once those are stored)
+        if (j > 0 && !(ok = warp_wait(B_OUTFREE, ph))) break;
 #pragma unroll
-          for (int e = 0; e < 32; e += PER) {
-            uint32_t w[8];
+        for (int i = 0; i < COLS; i += 32) {
+          float v[32];
+          tmem_ld32(tl + j + i, v);
+          tmem_wait_ld();
+          if (j + i == 32) {
+            tc_fence_before();
+            arrive(B_OFREE);
+          }
+          constexpr int W = 32 * sizeof(TO) / 4;  // words
+          uint32_t w[W];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              w[k] = sizeof(TO) == 2 ? pack_bf16x2(v[(e + 2 * k) % 32], v[(e + 2 * k + 1) % 32])
-                                     : __float_as_uint(v[e + k]);
-            st_global_32b(o + i + e, w);
+          for (int k = 0; k < W; ++k)
+            w[k] = sizeof(TO) == 2 ? pack_bf16x2(v[(2 * k) % 32], v[(2 * k + 1) % 32]) : __float_as_uint(v[k]);
+          if (whole) {
+#pragma unroll
+            for (int k = 0; k < W; k += 4)
+              *reinterpret_cast<uint4 *>(box + sw128_off(lane, i * (int)sizeof(TO) / 16 + k / 4)) =
+                  make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+          } else if (row < len) {  // the rows after belong to the next sequence
+            TO *o = static_cast<TO *>(p.out) + ((size_t)(u.t0 + c * CH + row) * p.Hv + u.h) * HD + 64 * hf + j + i;
+#pragma unroll
+            for (int k = 0; k < W; k += 4)
+              *reinterpret_cast<uint4 *>(o + k * 4 / (int)sizeof(TO)) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
           }
         }
+        fence_proxy_async_smem();
+        arrive(B_OUT);
       }
+      if (!ok) break;
     }
   }
   tc_fence_before();
@@ -585,7 +635,7 @@ scan_state_tc_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_cons
   extern __shared__ __align__(1024) unsigned char smem[];
   Unit u;
   if (!get_unit(p, blockIdx.x, u)) return;
-  if (u.last) return;  // no segment starts from its end
+  if (u.last && (u.first || !p.xf)) return;  // nothing starts from its end
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sb = smem_addr(smem);
   const int nch = (u.t1 - u.t0 + CH - 1) / CH;
@@ -726,9 +776,10 @@ scan_state_tc_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_cons
   }
 }
 
-// Tensor map of a packed [T, H, 128] bf16 tensor viewed as (d, head, token), box
-// 64 d x 1 head x 128 tokens, 128-byte swizzle.  Tokens past T read as zeros.
-bool make_map(CUtensorMap *m, const void *base, int H, int T) {
+// Tensor map of a packed [T, H, 128] bf16 (or fp32) tensor viewed as (d, head, token),
+// box 128 bytes of d x 1 head x `rows` tokens, 128-byte swizzle.  Tokens past T read as
+// zeros.
+bool make_map(CUtensorMap *m, const void *base, int H, int T, bool fp32 = false, int rows = CH) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     void *fn = nullptr;
     cudaDriverEntryPointQueryResult res;
@@ -739,9 +790,10 @@ bool make_map(CUtensorMap *m, const void *base, int H, int T) {
   }();
   if (!encode) return false;
   const cuuint64_t dims[3] = {HD, (cuuint64_t)H, (cuuint64_t)T};
-  const cuuint64_t strides[2] = {HD * 2, (cuuint64_t)H * HD * 2};
-  const cuuint32_t box[3] = {64, 1, CH}, elem[3] = {1, 1, 1};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, elem,
+  const cuuint64_t eb = fp32 ? 4 : 2;
+  const cuuint64_t strides[2] = {HD * eb, (cuuint64_t)H * HD * eb};
+  const cuuint32_t box[3] = {fp32 ? 32u : 64u, 1, (cuuint32_t)rows}, elem[3] = {1, 1, 1};
+  return encode(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, elem,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -750,12 +802,12 @@ bool make_map(CUtensorMap *m, const void *base, int H, int T) {
 
 bool scan_tc_supported(const Scan &p, int dtype) {
   return p.Da == HD && p.Dc == HD && dtype == GDN_DTYPE_BF16 && p.T > 0 &&
-         (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;  // 32-byte stores
+         p.T <= INT32_MAX - CH;
 }
 
 cudaError_t launch_scan_tc(const Scan &p, int units, int out_dtype, cudaStream_t stream) {
   static std::atomic<bool> f0[64], f1[64], f2[64], f3[64], f4[64];
-  CUtensorMap ma, mb, mc;
+  CUtensorMap ma, mb, mc, mo;
   if (!make_map(&mb, p.b, p.Hb, p.T) || !make_map(&mc, p.c, p.Hc, p.T)) return cudaErrorInvalidValue;
   cudaError_t e;
   if (!p.out) {
@@ -763,11 +815,12 @@ cudaError_t launch_scan_tc(const Scan &p, int units, int out_dtype, cudaStream_t
     scan_state_tc_kernel<<<(unsigned)units, NTHREADS, SMEM_STATE, stream>>>(mb, mc, p);
     return cudaGetLastError();
   }
-  if (!make_map(&ma, p.a, p.Ha, p.T)) return cudaErrorInvalidValue;
+  if (!make_map(&ma, p.a, p.Ha, p.T) || !make_map(&mo, p.out, p.Hv, p.T, out_dtype == GDN_DTYPE_FP32, 32))
+    return cudaErrorInvalidValue;
   auto go = [&](auto kern, std::atomic<bool>(&flags)[64]) {
     const cudaError_t r = set_smem_once(kern, SMEM_OUT, flags);
     if (r != cudaSuccess) return r;
-    kern<<<(unsigned)units, NTHREADS_O, SMEM_OUT, stream>>>(ma, mb, mc, p);
+    kern<<<(unsigned)units, NTHREADS_O, SMEM_OUT, stream>>>(ma, mb, mc, mo, p);
     return cudaGetLastError();
   };
   if (out_dtype == GDN_DTYPE_BF16)
