@@ -75,12 +75,18 @@ struct Layout {
   static constexpr int U = 0;                                  // [MP][LDU] over X, once X has been used
   static constexpr int O = MP * LDU * 4;                       // [MP][LDU]
   static constexpr int V = XB > 2 * O ? XB : 2 * O;            // [MP][DV] T
-  static constexpr int E = V + MP * DV * (int)sizeof(T);       // [MP][MP]
-  static constexpr int A = E + MP * MP * 4;                    // [MP][MP]  E_ij (k_j . k_i)
-  static constexpr int C = A + MP * MP * 4;                    // [MP][MP]  E_ij (k_j . q_i)
-  static constexpr int S = C + MP * MP * 4;                    // per-node scalars
-  static constexpr int BYTES = S + MP * 4 * 8;
+  // by node i and place s along its path (0: the parent), j the ancestor there
+  static constexpr int E = V + MP * DV * (int)sizeof(T);       // [MP][MP] fp32 E_ij
+  static constexpr int AC = E + MP * MP * 4;                   // [MP][MP] {E_ij (k_j . k_i), E_ij (k_j . q_i)}
+  static constexpr int IDX = AC + MP * MP * 8;                 // [MP][MP] bytes: j
+  static constexpr int S = IDX + MP * MP;                      // per-node scalars
+  static constexpr int BYTES = S + MP * 4 * 9;
 };
+
+__device__ __forceinline__ void cp_async_16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
 
 // One CTA per (sequence, value head).  S0 [k; q]^T (Dv x 2 M) and [k; q] k^T
 // (2 M x M) run on warp-level bf16 MMAs (fp32 accumulation); S0 goes straight
@@ -89,11 +95,12 @@ struct Layout {
 // operands use the same).  Values that bf16 does not hold are split into SP (S0)
 // or XP (fp32 k, q) bf16 terms; products of terms whose weight is below the last
 // term kept are dropped.  Then thread d owns value dimension d and solves for
-// u_i[d] node by node along each node's ancestors only, so that nothing of a
-// branch (a NaN, say) reaches another.
+// u_i[d] node by node along each node's path only, so that nothing of a branch (a
+// NaN, say) reaches another; a path's indices and factors lie in its order, four to
+// a load.  Every global load of the CTA is issued before the first is waited for.
 // Bound: HBM, one read of each state; the products are 4 M flops an element.
 template <typename T, typename ST, int SP, int XP, int DK, int DV, int MP>
-__global__ void __launch_bounds__(DV == 128 && MP == 64 ? 256 : 128, 2)
+__global__ void __launch_bounds__(DV == 128 && MP == 64 ? 256 : 128, MP <= 32 ? 3 : 2)
 decode_tree_kernel(const Params p) {
   pdl_wait();  // nothing is read before the previous kernel on the stream is done
   pdl_allow_next();
@@ -108,12 +115,14 @@ decode_tree_kernel(const Params p) {
   __nv_bfloat16 *X = reinterpret_cast<__nv_bfloat16 *>(smem + L::X);
   float *U = reinterpret_cast<float *>(smem + L::U), *O = reinterpret_cast<float *>(smem + L::O);
   T *V = reinterpret_cast<T *>(smem + L::V);
-  float *E = reinterpret_cast<float *>(smem + L::E), *A = reinterpret_cast<float *>(smem + L::A);
-  float *C = reinterpret_cast<float *>(smem + L::C);
+  float *E = reinterpret_cast<float *>(smem + L::E);
+  float2 *AC = reinterpret_cast<float2 *>(smem + L::AC);
+  unsigned char *idx = smem + L::IDX;
   unsigned long long *anc = reinterpret_cast<unsigned long long *>(smem + L::S);  // strict ancestors
   float *alpha = reinterpret_cast<float *>(smem + L::S + MP * 8), *bet = alpha + MP, *E0 = bet + MP;
-  float *rn = E0 + MP;  // [2 MP] 1/|k_i|, 1/|q_i| (1 for prepared inputs)
-  int32_t *par = reinterpret_cast<int32_t *>(rn + 2 * MP);
+  float *rn = E0 + MP;         // [2 MP] 1/|k_i|, 1/|q_i| (1 for prepared inputs)
+  float *cself = rn + 2 * MP;  // k_i . q_i
+  int32_t *par = reinterpret_cast<int32_t *>(cself + MP);
 
   const int b = blockIdx.x / p.Hv, h = blockIdx.x - b * p.Hv;
   const int j = h / (p.Hv / p.Hqk);
@@ -140,67 +149,90 @@ decode_tree_kernel(const Params p) {
 #pragma unroll
   for (int ks = 0; ks < PF; ++ks) load_ks(ks, ks);
 
-  // stage k, q (as bf16 terms), v and the gates; padding nodes as zeros
+  // stage k, q (as bf16 terms), v and the gates (rows past the last node as zeros)
+  const T *kb = static_cast<const T *>(p.k) + ((size_t)b * M * p.Hqk + j) * DK;
+  const T *qb = static_cast<const T *>(p.q) + ((size_t)b * M * p.Hqk + j) * DK;
+  const T *vb = static_cast<const T *>(p.v) + ((size_t)b * M * p.Hv + h) * DV;
+  constexpr int EV = 16 / (int)sizeof(T);  // elements of a 16-byte copy
+#pragma unroll
+  for (int x = tid; x < MP * (DV / EV); x += NT) {
+    const int i = x / (DV / EV), d = EV * (x - i * (DV / EV));
+    if (i < M) cp_async_16(V + i * DV + d, vb + (size_t)i * p.Hv * DV + d);
+  }
+  if (XP == 1) {  // bf16: the rows as they are
+#pragma unroll
+    for (int x = tid; x < 2 * MP * (DK / 8); x += NT) {
+      const int r = x / (DK / 8), d = 8 * (x - r * (DK / 8)), i = r < MP ? r : r - MP;
+      __nv_bfloat16 *dst = X + (size_t)r * L::LDX + d;
+      if (i < M) cp_async_16(dst, (r < MP ? kb : qb) + (size_t)i * p.Hqk * DK + d);
+      else *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
   int bad = 0;
   for (int i = tid; i < MP; i += NT) {
+    const size_t gi = ((size_t)b * M + i) * p.Hv + h;
     const int32_t pi = i < M ? p.parent[(size_t)b * M + i] : -2;
+    const float gv = i < M ? p.g[delta ? gi : (size_t)h] : 0.f, bv = i < M && delta ? p.beta[gi] : 1.f;
     par[i] = pi;
     bad |= pi >= i;
-    float a = 0.f, bt = 1.f;
-    if (i < M && pi >= -1) {
-      if (delta) {
-        const size_t gi = ((size_t)b * M + i) * p.Hv + h;
-        a = p.raw ? alpha_raw(p.g[gi]) : expf(p.g[gi]);
-        bt = p.raw ? beta_raw(p.beta[gi]) : p.beta[gi];
-      } else {
-        a = expf(fmaxf(p.g[h], rows::kDecayFloor));
+    alpha[i] = delta ? (p.raw ? alpha_raw(gv) : expf(gv)) : expf(fmaxf(gv, rows::kDecayFloor));
+    bet[i] = p.raw ? beta_raw(bv) : bv;
+  }
+  if (XP > 1) {  // fp32: as XP bf16 terms, four loads of a thread in flight
+    constexpr int N = 2 * MP * (DK / 4) / NT;
+#pragma unroll 1
+    for (int o = 0; o < N; o += 4) {
+      float y[4][4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int x = tid + (o + n) * NT, r = x / (DK / 4), d = 4 * (x - r * (DK / 4)), i = r < MP ? r : r - MP;
+        y[n][0] = y[n][1] = y[n][2] = y[n][3] = 0.f;
+        if (i < M) load4((r < MP ? kb : qb) + (size_t)i * p.Hqk * DK + d, y[n]);
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int x = tid + (o + n) * NT, r = x / (DK / 4), d = 4 * (x - r * (DK / 4));
+        uint32_t w[XP][2];
+        split4<XP>(y[n], w);
+#pragma unroll
+        for (int t = 0; t < XP; ++t)
+          *reinterpret_cast<uint2 *>(X + (size_t)(t * 2 * MP + r) * L::LDX + d) = make_uint2(w[t][0], w[t][1]);
       }
     }
-    alpha[i] = a;
-    bet[i] = bt;
   }
   __syncthreads();
   for (int i = tid; i < M; i += NT) bad |= par[i] >= 0 && par[i] < i && par[par[i]] < -1;
   if (__syncthreads_or(bad)) {  // a parent that is no earlier node of the tree
     if (tid == 0) report_status(p.status, GDN_ERR_INVALID_ARG);
+    asm volatile("cp.async.wait_all;" ::: "memory");
     return;
-  }
-  for (int x = tid; x < 2 * MP * (DK / 4); x += NT) {
-    const int r = x / (DK / 4), d = 4 * (x - r * (DK / 4));
-    const int i = r < MP ? r : r - MP;
-    float y[4] = {0.f, 0.f, 0.f, 0.f};
-    if (par[i] >= -1)
-      load4(static_cast<const T *>(r < MP ? p.k : p.q) + (((size_t)b * M + i) * p.Hqk + j) * DK + d, y);
-    uint32_t w[XP][2];
-    split4<XP>(y, w);
-#pragma unroll
-    for (int t = 0; t < XP; ++t)
-      *reinterpret_cast<uint2 *>(X + (size_t)(t * 2 * MP + r) * L::LDX + d) = make_uint2(w[t][0], w[t][1]);
-  }
-  for (int x = tid; x < MP * (DV / 4); x += NT) {
-    const int i = x / (DV / 4), d = 4 * (x - i * (DV / 4));
-    float y[4] = {0.f, 0.f, 0.f, 0.f};
-    if (par[i] >= -1) load4(static_cast<const T *>(p.v) + (((size_t)b * M + i) * p.Hv + h) * DV + d, y);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) V[i * DV + d + e] = from_f32<T>(y[e]);
   }
   // paths: E_ij, E_i0 and the set of strict ancestors of each node
   for (int i = tid; i < MP; i += NT) {
     unsigned long long m = 0;
     float e = alpha[i];
-    E[i * MP + i] = 1.f;
-    for (int a = par[i]; a >= 0; a = par[a]) {
+    int s = 0, a = par[i];
+    for (; a >= 0; a = par[a], ++s) {
       m |= 1ull << a;
-      E[i * MP + a] = e;
+      E[i * MP + s] = e;
+      idx[i * MP + s] = (unsigned char)a;
       e *= alpha[a];
+    }
+    // to a multiple of four: the parent again, with factors of zero
+    for (; s & 3; ++s) {
+      idx[i * MP + s] = idx[i * MP];
+      AC[i * MP + s] = make_float2(0.f, 0.f);
     }
     anc[i] = m;
     E0[i] = e;
+    rn[i] = rn[MP + i] = 1.f;
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  for (int r = warp; r < 2 * MP; r += NW) {
-    float ss = 0.f;
-    if (p.raw)
+  if (p.raw) {
+    for (int r = warp; r < 2 * MP; r += NW) {
+      float ss = 0.f;
       for (int d = lane; d < DK; d += 32) {
         float y = 0.f;
 #pragma unroll
@@ -208,16 +240,17 @@ decode_tree_kernel(const Params p) {
         ss = fmaf(y, y, ss);
       }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    if (lane == 0) rn[r] = p.raw ? inv_norm(ss) : 1.f;
+      for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+      if (lane == 0) rn[r] = inv_norm(ss);
+    }
+    __syncthreads();
   }
-  __syncthreads();
 
   // fragment words of X: rows r (A: r = tile row; B: r = node), K positions 16 ks + 4 tig
   auto xw = [&](int t, int r, int ks) {
     return *reinterpret_cast<const uint2 *>(X + (size_t)(t * 2 * MP + r) * L::LDX + 16 * ks + 4 * tig);
   };
-  // [k; q] k^T -> A, C (ancestors only)
+  // [k; q] k^T -> AC (ancestors only)
   for (int mt = warp; mt < 2 * MP / 16; mt += NW) {
     float acc[MP / 8][4] = {};
 #pragma unroll 2
@@ -244,9 +277,13 @@ decode_tree_kernel(const Params p) {
       for (int e = 0; e < 4; ++e) {
         const int r = 16 * mt + gid + 8 * (e >> 1), c = 8 * n + 2 * tig + (e & 1);
         const int i = r < MP ? r : r - MP;
-        const bool on = (anc[i] >> c & 1) || (i == c && r >= MP);
-        const float y = on ? acc[n][e] * E[i * MP + c] * (rn[r] * rn[c]) : 0.f;
-        (r < MP ? A : C)[i * MP + c] = y;
+        const float y = acc[n][e] * (rn[r] * rn[c]);
+        if (anc[i] >> c & 1) {
+          const int s = i * MP + __popcll(anc[i] >> c) - 1;  // its place on the path
+          (r < MP ? AC[s].x : AC[s].y) = E[s] * y;
+        } else if (i == c && r >= MP) {
+          cself[i] = y;
+        }
       }
   }
   // S0 [k; q]^T
@@ -294,22 +331,51 @@ decode_tree_kernel(const Params p) {
 
   if (tid < DV) {
     const int d = tid;
+    // what node i needs that does not come from other nodes, read one node ahead
+    struct Node {
+      int par, n;
+      float r, y, bet, cself;
+      uchar4 a;
+      float4 f0, f1;
+    };
+    auto read = [&](int i) {
+      Node x;
+      x.par = par[i];
+      x.n = __popcll(anc[i]);
+      x.r = to_f32(V[i * DV + d]);
+      if (delta) x.r -= U[i * L::LDU + d];
+      x.y = O[i * L::LDU + d];
+      x.bet = bet[i];
+      x.cself = cself[i];
+      x.a = *reinterpret_cast<const uchar4 *>(idx + i * MP);
+      x.f0 = *reinterpret_cast<const float4 *>(AC + i * MP);
+      x.f1 = *reinterpret_cast<const float4 *>(AC + i * MP + 2);
+      return x;
+    };
+    const size_t ostep = (size_t)p.Hv * DV;
+    const size_t off = ((size_t)b * M * p.Hv + h) * DV + d;
+    Node next = read(0);
+#pragma unroll 1
     for (int i = 0; i < M; ++i) {
-      if (par[i] < -1) continue;  // padding node: its output row stays
-      float r = to_f32(V[i * DV + d]), y = O[i * L::LDU + d];
-      if (delta) r -= U[i * L::LDU + d];
-      for (unsigned long long m = anc[i]; m; m &= m - 1) {
-        const int a = __ffsll((long long)m) - 1;
-        const float u = U[a * L::LDU + d];
-        if (delta) r = fmaf(-A[i * MP + a], u, r);
-        y = fmaf(C[i * MP + a], u, y);
-      }
-      const float u = delta ? bet[i] * r : r;
+      const Node x = next;
+      if (i + 1 < M) next = read(i + 1);
+      if (x.par < -1) continue;  // padding node: its output row stays
+      float r = x.r, y = x.y;
+      auto add = [&](const uchar4 &a, const float4 &f0, const float4 &f1) {
+        const float u0 = U[a.x * L::LDU + d], u1 = U[a.y * L::LDU + d];
+        const float u2 = U[a.z * L::LDU + d], u3 = U[a.w * L::LDU + d];
+        if (delta) r -= fmaf(f0.x, u0, f0.z * u1) + fmaf(f1.x, u2, f1.z * u3);
+        y += fmaf(f0.y, u0, f0.w * u1) + fmaf(f1.y, u2, f1.w * u3);
+      };
+      if (x.n > 0) add(x.a, x.f0, x.f1);
+      for (int s = 4; s < x.n; s += 4)
+        add(*reinterpret_cast<const uchar4 *>(idx + i * MP + s), *reinterpret_cast<const float4 *>(AC + i * MP + s),
+            *reinterpret_cast<const float4 *>(AC + i * MP + s + 2));
+      const float u = delta ? x.bet * r : r;
       U[i * L::LDU + d] = u;
-      y = p.scale * fmaf(C[i * MP + i], u, y);
-      const size_t off = (((size_t)b * M + i) * p.Hv + h) * DV + d;
-      if (p.o_bf16) static_cast<__nv_bfloat16 *>(p.o)[off] = __float2bfloat16_rn(y);
-      else static_cast<float *>(p.o)[off] = y;
+      y = p.scale * fmaf(x.cself, u, y);
+      if (p.o_bf16) static_cast<__nv_bfloat16 *>(p.o)[off + i * ostep] = __float2bfloat16_rn(y);
+      else static_cast<float *>(p.o)[off + i * ostep] = y;
     }
   }
 }

@@ -517,7 +517,7 @@ int32_t gdn_linear_decode_tokens(const void *q, const void *k, const void *v, co
  *   v           [batch, nodes, Hv, Dv]    dtype
  *   g, beta     [batch, nodes, Hv]        fp32; or beta NULL and g [Hv]
  *   parent      [batch, nodes] int32, device.  An entry below -1 marks a padding
- *               node: its q, k, v are not read and its o is left untouched.
+ *               node: its q, k, v, g, beta have no effect and its o is left untouched.
  *   state       [num_slots, Hv, Dv, Dk]   state_dtype, pool read
  *   src_slot    [batch] int32, device: slot of sequence b; NULL means slot b.  A
  *               negative entry marks padding: its o is left untouched.
