@@ -80,7 +80,7 @@ struct Layout {
   static constexpr int AC = E + MP * MP * 4;                   // [MP][MP] {E_ij (k_j . k_i), E_ij (k_j . q_i)}
   static constexpr int IDX = AC + MP * MP * 8;                 // [MP][MP] bytes: j
   static constexpr int S = IDX + MP * MP;                      // per-node scalars
-  static constexpr int BYTES = S + MP * 4 * 9;
+  static constexpr int BYTES = S + MP * 4 * 11 + 16;
 };
 
 __device__ __forceinline__ void cp_async_16(void *dst, const void *src) {
@@ -94,10 +94,10 @@ __device__ __forceinline__ void cp_async_16(void *dst, const void *src) {
 // lane owns (the order of K within a 16-wide step is free as long as both
 // operands use the same).  Values that bf16 does not hold are split into SP (S0)
 // or XP (fp32 k, q) bf16 terms; products of terms whose weight is below the last
-// term kept are dropped.  Then thread d owns value dimension d and solves for
-// u_i[d] node by node along each node's path only, so that nothing of a branch (a
-// NaN, say) reaches another; a path's indices and factors lie in its order, four to
-// a load.  Every global load of the CTA is issued before the first is waited for.
+// term kept are dropped.  Then u is solved for depth by depth, a warp for a node
+// (nodes of one depth do not depend on one another), along the node's path only, so
+// that nothing of a branch (a NaN, say) reaches another; a path's indices and factors
+// lie in its order, four to a load.  Every global load of the CTA is issued before the first is waited for.
 // Bound: HBM, one read of each state; the products are 4 M flops an element.
 template <typename T, typename ST, int SP, int XP, int DK, int DV, int MP>
 __global__ void __launch_bounds__(DV == 128 && MP == 64 ? 256 : 128, MP <= 32 ? 3 : 2)
@@ -123,6 +123,9 @@ decode_tree_kernel(const Params p) {
   float *rn = E0 + MP;         // [2 MP] 1/|k_i|, 1/|q_i| (1 for prepared inputs)
   float *cself = rn + 2 * MP;  // k_i . q_i
   int32_t *par = reinterpret_cast<int32_t *>(cself + MP);
+  int32_t *order = par + MP;                   // the nodes by depth
+  int32_t *level = order + MP;                 // [MP + 1] first place of each depth; then the end
+  int32_t *nodes = level + MP + 1;             // how many there are
 
   const int b = blockIdx.x / p.Hv, h = blockIdx.x - b * p.Hv;
   const int j = h / (p.Hv / p.Hqk);
@@ -230,6 +233,28 @@ decode_tree_kernel(const Params p) {
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
+  if (warp == NW - 1) {  // places by depth
+    constexpr int PL = (MP + 31) / 32;
+    int depth[PL], base = 0, todo = 0;
+#pragma unroll
+    for (int n = 0; n < PL; ++n) {
+      const int i = lane + 32 * n;
+      depth[n] = i < M && par[i] >= -1 ? __popcll(anc[i]) : -1;
+      todo += __popc(__ballot_sync(0xffffffffu, depth[n] >= 0));
+    }
+    for (int l = 0; base < todo; ++l) {
+      if (lane == 0) level[l] = base;
+#pragma unroll
+      for (int n = 0; n < PL; ++n) {
+        const unsigned m = __ballot_sync(0xffffffffu, depth[n] == l);
+        if (depth[n] == l) order[base + __popc(m & ((1u << lane) - 1))] = lane + 32 * n;
+        base += __popc(m);
+      }
+      if (lane == 0) level[l + 1] = base;
+    }
+    if (lane == 0 && todo == 0) level[0] = 0;
+    if (lane == 0) *nodes = todo;
+  }
   if (p.raw) {
     for (int r = warp; r < 2 * MP; r += NW) {
       float ss = 0.f;
@@ -329,54 +354,49 @@ decode_tree_kernel(const Params p) {
       }
   __syncthreads();
 
-  if (tid < DV) {
-    const int d = tid;
-    // what node i needs that does not come from other nodes, read one node ahead
-    struct Node {
-      int par, n;
-      float r, y, bet, cself;
-      uchar4 a;
-      float4 f0, f1;
-    };
-    auto read = [&](int i) {
-      Node x;
-      x.par = par[i];
-      x.n = __popcll(anc[i]);
-      x.r = to_f32(V[i * DV + d]);
-      if (delta) x.r -= U[i * L::LDU + d];
-      x.y = O[i * L::LDU + d];
-      x.bet = bet[i];
-      x.cself = cself[i];
-      x.a = *reinterpret_cast<const uchar4 *>(idx + i * MP);
-      x.f0 = *reinterpret_cast<const float4 *>(AC + i * MP);
-      x.f1 = *reinterpret_cast<const float4 *>(AC + i * MP + 2);
-      return x;
-    };
-    const size_t ostep = (size_t)p.Hv * DV;
-    const size_t off = ((size_t)b * M * p.Hv + h) * DV + d;
-    Node next = read(0);
-#pragma unroll 1
-    for (int i = 0; i < M; ++i) {
-      const Node x = next;
-      if (i + 1 < M) next = read(i + 1);
-      if (x.par < -1) continue;  // padding node: its output row stays
-      float r = x.r, y = x.y;
-      auto add = [&](const uchar4 &a, const float4 &f0, const float4 &f1) {
-        const float u0 = U[a.x * L::LDU + d], u1 = U[a.y * L::LDU + d];
-        const float u2 = U[a.z * L::LDU + d], u3 = U[a.w * L::LDU + d];
-        if (delta) r -= fmaf(f0.x, u0, f0.z * u1) + fmaf(f1.x, u2, f1.z * u3);
-        y += fmaf(f0.y, u0, f0.w * u1) + fmaf(f1.y, u2, f1.w * u3);
-      };
-      if (x.n > 0) add(x.a, x.f0, x.f1);
-      for (int s = 4; s < x.n; s += 4)
-        add(*reinterpret_cast<const uchar4 *>(idx + i * MP + s), *reinterpret_cast<const float4 *>(AC + i * MP + s),
-            *reinterpret_cast<const float4 *>(AC + i * MP + s + 2));
-      const float u = delta ? x.bet * r : r;
-      U[i * L::LDU + d] = u;
-      y = p.scale * fmaf(x.cself, u, y);
-      if (p.o_bf16) static_cast<__nv_bfloat16 *>(p.o)[off + i * ostep] = __float2bfloat16_rn(y);
-      else static_cast<float *>(p.o)[off + i * ostep] = y;
+  const int total = *nodes, d = 4 * lane;
+  for (int l = 0, begin = 0; begin < total; ++l) {
+    const int end = level[l + 1];
+    for (int at = begin + warp; at < end; at += NW) {
+      const int i = order[at];
+      if (d < DV) {
+        float r[4], y[4], u[4];
+        load4(V + i * DV + d, r);
+        load4(O + i * L::LDU + d, y);
+        load4(U + i * L::LDU + d, u);
+        if (delta)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) r[e] -= u[e];
+        for (int s = 0; s < l; s += 4) {  // l: the length of the path before i
+          const uchar4 a = *reinterpret_cast<const uchar4 *>(idx + i * MP + s);
+          const float4 f0 = *reinterpret_cast<const float4 *>(AC + i * MP + s);
+          const float4 f1 = *reinterpret_cast<const float4 *>(AC + i * MP + s + 2);
+          float ua[4][4];
+          load4(U + a.x * L::LDU + d, ua[0]);
+          load4(U + a.y * L::LDU + d, ua[1]);
+          load4(U + a.z * L::LDU + d, ua[2]);
+          load4(U + a.w * L::LDU + d, ua[3]);
+          const float fa[4] = {f0.x, f0.z, f1.x, f1.z}, fc[4] = {f0.y, f0.w, f1.y, f1.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (delta) r[e] = fmaf(-fa[k], ua[k][e], r[e]);
+              y[e] = fmaf(fc[k], ua[k][e], y[e]);
+            }
+        }
+        const float bt = delta ? bet[i] : 1.f, cs = cself[i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          u[e] = bt * r[e];
+          y[e] = p.scale * fmaf(cs, u[e], y[e]);
+        }
+        *reinterpret_cast<float4 *>(U + i * L::LDU + d) = make_float4(u[0], u[1], u[2], u[3]);
+        store_state4(p.o, (((size_t)b * M + i) * p.Hv + h) * DV + d, p.o_bf16, y);
+      }
     }
+    begin = end;
+    __syncthreads();  // the next depth reads these u
   }
 }
 
