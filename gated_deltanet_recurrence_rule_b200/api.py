@@ -113,14 +113,26 @@ def _check(status: int, what: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(device.index)  # (current_stream(device) makes a Stream, 2 us)
+
+
+def _launch(device, fn, *args):
+    """Call a libgdn function with ``device`` current; its stream goes last."""
+    if torch.cuda.current_device() == device.index:
+        return fn(*args, _stream(device))
+    with torch.cuda.device(device):
+        return fn(*args, _stream(device))
 
 
 def _require(t, name, device, dtype=None, shape=None):
+    # the usual case in one expression: these checks are most of a small call's time
+    if (type(t) is torch.Tensor and t.is_contiguous() and (shape is None or t.shape == shape)
+            and (dtype is None or t.dtype is dtype) and t.device == device):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
@@ -374,32 +386,32 @@ def _check_tokens(q, k, v, what):
         raise ValueError(f"{what} runs on a CUDA device only")
     if k.dim() != 4 or not isinstance(v, torch.Tensor) or v.dim() != 4:
         raise ValueError(f"{what}: k must be [B, tokens, Hqk, Dk] and v [B, tokens, Hv, Dv]")
-    B, Tn, Hqk, Dk = k.shape
-    Hv, Dv = v.shape[2], v.shape[3]
-    if k.dtype not in _DTYPE_CODE:
-        raise ValueError(f"unsupported dtype {k.dtype}")
+    dev, dt, shape = k.device, k.dtype, k.shape
+    B, Tn, Hqk, Dk = shape
+    _, _, Hv, Dv = v.shape
+    if dt not in _DTYPE_CODE:
+        raise ValueError(f"unsupported dtype {dt}")
     if q is not None:
-        _require(q, "q", k.device, k.dtype, (B, Tn, Hqk, Dk))
-    _require(k, "k", k.device, k.dtype)
-    _require(v, "v", k.device, k.dtype, (B, Tn, Hv, Dv))
-    return k.device, B, Tn, Hqk, Hv, Dk, Dv
+        _require(q, "q", dev, dt, shape)
+    _require(k, "k", dev, dt)
+    _require(v, "v", dev, dt, (B, Tn, Hv, Dv))
+    return dev, B, Tn, Hqk, Hv, Dk, Dv
 
 
 def _check_pool(state_in, state_out, dev, Hv, Dv, Dk):
     """Checks of the state pools; returns (num_slots, state dtype)."""
     if not isinstance(state_in, torch.Tensor) or state_in.dtype not in _DTYPE_CODE:
         raise ValueError("the state pool must be a bf16 or fp32 tensor")
-    shape = (state_in.shape[0] if state_in.dim() else 0, Hv, Dv, Dk)
-    _require(state_in, "state_in", dev, state_in.dtype, shape)
-    if state_out is not None:
-        _require(state_out, "state_out", dev, state_in.dtype, shape)
-    return shape[0], state_in.dtype
+    dt, shape = state_in.dtype, (state_in.shape[0] if state_in.dim() else 0, Hv, Dv, Dk)
+    _require(state_in, "state_in", dev, dt, shape)
+    if state_out is not None and state_out is not state_in:
+        _require(state_out, "state_out", dev, dt, shape)
+    return shape[0], dt
 
 
-def _check_ints(dev, **tensors):
-    for name, (t, shape) in tensors.items():
-        if t is not None:
-            _require(t, name, dev, torch.int32, shape)
+def _check_ints(dev, name, t, n):
+    if t is not None:
+        _require(t, name, dev, torch.int32, (n,))
 
 
 def _output(o, o_dtype, shape, dev):
@@ -428,14 +440,14 @@ def _check_packed(q, k, v, g, cu_seqlens, what):
         raise ValueError(f"{what} runs on a CUDA device only")
     if q.dim() != 3 or not isinstance(v, torch.Tensor) or v.dim() != 3:
         raise ValueError(f"{what}: q must be [T, Hqk, Dk] and v [T, Hv, Dv]")
-    dev = q.device
-    T, Hqk, Dk = q.shape
-    Hv, Dv = v.shape[1], v.shape[2]
-    if q.dtype not in _DTYPE_CODE:
-        raise ValueError(f"unsupported dtype {q.dtype}")
-    _require(q, "q", dev, q.dtype)
-    _require(k, "k", dev, q.dtype, (T, Hqk, Dk))
-    _require(v, "v", dev, q.dtype, (T, Hv, Dv))
+    dev, dt, shape = q.device, q.dtype, q.shape
+    T, Hqk, Dk = shape
+    _, Hv, Dv = v.shape
+    if dt not in _DTYPE_CODE:
+        raise ValueError(f"unsupported dtype {dt}")
+    _require(q, "q", dev, dt)
+    _require(k, "k", dev, dt, shape)
+    _require(v, "v", dev, dt, (T, Hv, Dv))
     _require(g, "g", dev, torch.float32, (Hv,))
     if cu_seqlens is None:
         cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=dev)
@@ -445,9 +457,9 @@ def _check_packed(q, k, v, g, cu_seqlens, what):
     return dev, T, cu_seqlens.numel() - 1, Hqk, Hv, Dk, Dv, cu_seqlens
 
 
-def _workspace(workspace, need, dev):
-    if workspace is None:
-        workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=dev)
+def _workspace(workspace, dev, *sizes):
+    if workspace is None:  # (a given one's size is checked by the library)
+        workspace = torch.zeros(max(linear_prefill_workspace_size(*sizes), 256), dtype=torch.uint8, device=dev)
     _require(workspace, "workspace", dev, torch.uint8)
     return workspace
 
@@ -477,13 +489,11 @@ def linear_prefill(q, k, v, g, cu_seqlens=None, initial_state=None, output_final
     if final_state is not None:
         _require(final_state, "final_state", dev, sdt, sshape)
     o = _output(o, o_dtype, (T, Hv, Dv), dev)
-    with torch.cuda.device(dev):
-        need = linear_prefill_workspace_size(N, T, Hqk, Hv, Dk, Dv, q.dtype)
-        workspace = _workspace(workspace, need, dev)
-        st = lib.gdn_linear_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(cu_seqlens), N, T, Hqk, Hv, Dk,
-                                    Dv, _DTYPE_CODE[q.dtype], _DTYPE_CODE[o.dtype], _DTYPE_CODE[sdt],
-                                    float(scale), _ptr(initial_state), _ptr(final_state), _ptr(o),
-                                    _ptr(workspace), workspace.numel(), _stream(dev))
+    workspace = _workspace(workspace, dev, N, T, Hqk, Hv, Dk, Dv, q.dtype)
+    st = _launch(dev, lib.gdn_linear_prefill, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(cu_seqlens), N, T, Hqk, Hv, Dk,
+                                Dv, _DTYPE_CODE[q.dtype], _DTYPE_CODE[o.dtype], _DTYPE_CODE[sdt],
+                                float(scale), _ptr(initial_state), _ptr(final_state), _ptr(o),
+                                _ptr(workspace), workspace.numel())
     _check(st, "gdn_linear_prefill")
     return o, final_state
 
@@ -503,14 +513,12 @@ def linear_prefill_backward(q, k, v, g, d_o, cu_seqlens=None, initial_state=None
             _require(t, name, dev, torch.float32, sshape)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     ds0 = torch.empty(sshape, dtype=torch.float32, device=dev) if want_d_initial_state else None
-    with torch.cuda.device(dev):
-        need = linear_prefill_workspace_size(N, T, Hqk, Hv, Dk, Dv, q.dtype, backward=True)
-        workspace = _workspace(workspace, need, dev)
-        st = lib.gdn_linear_prefill_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(cu_seqlens), N, T, Hqk,
-                                             Hv, Dk, Dv, _DTYPE_CODE[q.dtype], float(scale),
-                                             _ptr(initial_state), _ptr(d_o), _ptr(d_final_state), _ptr(dq),
-                                             _ptr(dk), _ptr(dv), _ptr(ds0), _ptr(workspace),
-                                             workspace.numel(), _stream(dev))
+    workspace = _workspace(workspace, dev, N, T, Hqk, Hv, Dk, Dv, q.dtype, True)
+    st = _launch(dev, lib.gdn_linear_prefill_backward, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(cu_seqlens), N, T, Hqk,
+                                         Hv, Dk, Dv, _DTYPE_CODE[q.dtype], float(scale),
+                                         _ptr(initial_state), _ptr(d_o), _ptr(d_final_state), _ptr(dq),
+                                         _ptr(dk), _ptr(dv), _ptr(ds0), _ptr(workspace),
+                                         workspace.numel())
     _check(st, "gdn_linear_prefill_backward")
     return dq, dk, dv, ds0
 
@@ -529,14 +537,15 @@ def linear_decode_tokens(q, k, v, g, state_in, state_out=None, src_slot=None, ds
     if state_out is None:
         state_out = state_in
     num_slots, sdt = _check_pool(state_in, state_out, dev, Hv, Dv, Dk)
-    _check_ints(dev, src_slot=(src_slot, (B,)), dst_slot=(dst_slot, (B,)), device_status=(device_status, (1,)))
+    _check_ints(dev, "src_slot", src_slot, B)
+    _check_ints(dev, "dst_slot", dst_slot, B)
+    _check_ints(dev, "device_status", device_status, 1)
     o = _output(o, o_dtype, (B, Tn, Hv, Dv), dev)
-    with torch.cuda.device(dev):
-        st = lib.gdn_linear_decode_tokens(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state_in),
-                                          _ptr(state_out), _ptr(src_slot), _ptr(dst_slot), num_slots,
-                                          _ptr(o), B, Tn, Hqk, Hv, Dk, Dv, _DTYPE_CODE[k.dtype],
-                                          _DTYPE_CODE[o.dtype], _DTYPE_CODE[sdt], float(scale),
-                                          _ptr(device_status), _stream(dev))
+    st = _launch(dev, lib.gdn_linear_decode_tokens, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state_in),
+                                      _ptr(state_out), _ptr(src_slot), _ptr(dst_slot), num_slots,
+                                      _ptr(o), B, Tn, Hqk, Hv, Dk, Dv, _DTYPE_CODE[k.dtype],
+                                      _DTYPE_CODE[o.dtype], _DTYPE_CODE[sdt], float(scale),
+                                      _ptr(device_status))
     _check(st, "gdn_linear_decode_tokens")
     return o
 
@@ -567,14 +576,14 @@ def decode_tree(q, k, v, g, beta, parent, state, src_slot=None, o=None, scale=1.
     _check_gates(g, beta, raw_inputs, dev, B, M, Hv)
     _require(parent, "parent", dev, torch.int32, (B, M))
     num_slots, sdt = _check_pool(state, None, dev, Hv, Dv, Dk)
-    _check_ints(dev, src_slot=(src_slot, (B,)), device_status=(device_status, (1,)))
+    _check_ints(dev, "src_slot", src_slot, B)
+    _check_ints(dev, "device_status", device_status, 1)
     o = _output(o, o_dtype, (B, M, Hv, Dv), dev)
-    with torch.cuda.device(dev):
-        st = lib.gdn_decode_tree(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(parent), _ptr(state),
-                                 _ptr(src_slot), num_slots, _ptr(o), B, M, Hqk, Hv, Dk, Dv,
-                                 _DTYPE_CODE[k.dtype], _DTYPE_CODE[o.dtype], _DTYPE_CODE[sdt],
-                                 GDN_INPUT_RAW if raw_inputs else GDN_INPUT_PREPARED, float(scale),
-                                 _ptr(device_status), _stream(dev))
+    st = _launch(dev, lib.gdn_decode_tree, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(parent), _ptr(state),
+                             _ptr(src_slot), num_slots, _ptr(o), B, M, Hqk, Hv, Dk, Dv,
+                             _DTYPE_CODE[k.dtype], _DTYPE_CODE[o.dtype], _DTYPE_CODE[sdt],
+                             GDN_INPUT_RAW if raw_inputs else GDN_INPUT_PREPARED, float(scale),
+                             _ptr(device_status))
     _check(st, "gdn_decode_tree")
     return o
 
@@ -593,13 +602,13 @@ def tree_commit(k, v, g, beta, parent, accept, state_in, state_out=None, src_slo
     if state_out is None:
         state_out = state_in
     num_slots, sdt = _check_pool(state_in, state_out, dev, Hv, Dv, Dk)
-    _check_ints(dev, src_slot=(src_slot, (B,)), dst_slot=(dst_slot, (B,)), device_status=(device_status, (1,)))
-    with torch.cuda.device(dev):
-        st = lib.gdn_tree_commit(_ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(parent), _ptr(accept),
-                                 _ptr(state_in), _ptr(state_out), _ptr(src_slot), _ptr(dst_slot), num_slots,
-                                 B, M, Hqk, Hv, Dk, Dv, _DTYPE_CODE[k.dtype], _DTYPE_CODE[sdt],
-                                 GDN_INPUT_RAW if raw_inputs else GDN_INPUT_PREPARED, _ptr(device_status),
-                                 _stream(dev))
+    _check_ints(dev, "src_slot", src_slot, B)
+    _check_ints(dev, "dst_slot", dst_slot, B)
+    _check_ints(dev, "device_status", device_status, 1)
+    st = _launch(dev, lib.gdn_tree_commit, _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(parent), _ptr(accept),
+                             _ptr(state_in), _ptr(state_out), _ptr(src_slot), _ptr(dst_slot), num_slots,
+                             B, M, Hqk, Hv, Dk, Dv, _DTYPE_CODE[k.dtype], _DTYPE_CODE[sdt],
+                             GDN_INPUT_RAW if raw_inputs else GDN_INPUT_PREPARED, _ptr(device_status))
     _check(st, "gdn_tree_commit")
     return state_out
 
