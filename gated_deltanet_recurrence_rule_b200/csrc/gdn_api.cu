@@ -412,7 +412,7 @@ int32_t check_linear(const void *q, const void *k, const void *v, const float *g
   }
   // grid-size limits of the launches: 16 tiles of every (segment, head) state, and
   // a thread for 4 elements of every (token, head) row
-  const int64_t segments = total_tokens / 512 + num_seqs;
+  const int64_t segments = total_tokens / 128 + num_seqs;
   if (segments * num_v_heads * 16 > INT32_MAX || total_tokens * num_qk_heads / 8 > INT32_MAX)
     return GDN_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256) ||

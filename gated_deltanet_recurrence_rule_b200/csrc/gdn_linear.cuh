@@ -106,7 +106,7 @@ __device__ __forceinline__ float start_state(const Scan &p, const Unit &w, int i
 
 // W consecutive elements of row i of it (j a multiple of 4).
 template <int W>
-__device__ __forceinline__ void load_start(const Scan &p, const Unit &w, float, int i, int j, float *x) {
+__device__ __forceinline__ void load_start(const Scan &p, const Unit &w, int i, int j, float *x) {
   if (!w.first || !w.last) {
     const float *s = p.seg_state + (((size_t)w.seg * p.Hv + w.h) * p.Dc + i) * p.Da + j;
 #pragma unroll
@@ -124,7 +124,7 @@ __device__ __forceinline__ void load_start(const Scan &p, const Unit &w, float, 
 // ---- host ----
 // The CUDA-core-and-mma.sync form, every type and head dim (gdn_linear_scan.cu).
 cudaError_t launch_scan(const Scan &p, int units, int dtype, int out_dtype, cudaStream_t stream);
-// The tcgen05 form (gdn_linear_tc.cu): bf16 operands, Da = Dc = 128.  Its states
+// The tcgen05 form (gdn_linear_tc.cu): bf16 operands.  Its states
 // are exact to fp32; its outputs carry the roundings of bf16 operands, whatever type
 // they are stored in.
 bool scan_tc_supported(const Scan &p, int dtype);

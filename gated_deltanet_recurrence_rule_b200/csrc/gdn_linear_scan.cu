@@ -387,12 +387,22 @@ namespace {
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// Segment length in tokens (a multiple of 128, the longest chunk): the share of one
-// multiprocessor, so that a single sequence makes one wave of units and only a
-// sequence longer than that share is cut (the cut costs a second reading of b and c).
-int segment_len(int64_t T, int Hv) {
-  const int64_t units = std::max<int64_t>(1, sm_count() / Hv);  // segments of one wave
-  return (int)std::max<int64_t>(512, round_up((size_t)((T + units - 1) / units), 128));
+// Segment length in tokens.  tcgen05 form: a chunk of 128 tokens takes about 2.8 us of
+// one multiprocessor, 1.4 us more where the sequence is cut (its states), and cutting
+// costs about 27 us of launches, starts and state moves; so a sequence is cut into
+// one segment for each multiprocessor of its head's share, if that saves more than it
+// costs (prefill of 8192 tokens, 48 heads: 155 us in 3 segments, about 190 in one).
+// The other form: chunks of 64 tokens take several times as long, so segments go down
+// to two chunks as long as there are multiprocessors.
+int segment_len(int64_t T, int Hv, int Dv, bool tc) {
+  if (tc) {
+    const double s = std::max(1, sm_count() / Hv);  // segments of one wave
+    const double chunks = (double)((T + 127) / 128);
+    if (chunks * (2.8 - (2.8 + 1.4) / s) <= 27.0) return (int)std::max<int64_t>(128, round_up((size_t)T, 128));
+    return (int)round_up((size_t)((T + (int64_t)s - 1) / (int64_t)s), 128);
+  }
+  const int64_t units = std::max<int64_t>(1, 2 * sm_count() / (Hv * (Dv / DCT)));
+  return (int)std::max<int64_t>(128, round_up((size_t)((T + units - 1) / units), 64));
 }
 
 struct Layout {
@@ -401,9 +411,9 @@ struct Layout {
   size_t first_seg, seg_seq, order, nat, tr, part, total;
 };
 
-Layout layout(int64_t N, int64_t T, int Hqk, int Hv, int Dk, int Dv, bool backward) {
+Layout layout(int64_t N, int64_t T, int Hqk, int Hv, int Dk, int Dv, bool tc, bool backward) {
   Layout l;
-  l.L = segment_len(T, Hv);
+  l.L = segment_len(T, Hv, Dv, tc);
   const bool one = T <= l.L;
   l.max_seg = one ? N : T / l.L + N;
   size_t at = kWorkspaceHeaderBytes;
@@ -428,18 +438,20 @@ Layout layout(int64_t N, int64_t T, int Hqk, int Hv, int Dk, int Dv, bool backwa
 }  // namespace lin
 
 size_t linear_workspace_bytes(int64_t N, int64_t T, int Hqk, int Hv, int Dk, int Dv, bool backward) {
-  return lin::layout(N, T, Hqk, Hv, Dk, Dv, backward).total;
+  // of both forms: the output's type, which decides between them, is not known here
+  return std::max(lin::layout(N, T, Hqk, Hv, Dk, Dv, true, backward).total,
+                  lin::layout(N, T, Hqk, Hv, Dk, Dv, false, backward).total);
 }
 
 namespace lin {
 
-// result_dtype: the type the caller's result ends up in.  Where that is bf16 (or
-// only states are wanted) the tcgen05 form serves.
-static cudaError_t run_scan(const Scan &p, int units, int dtype, int out_dtype, int result_dtype,
-                            cudaStream_t stream) {
-  if ((!p.out || result_dtype == GDN_DTYPE_BF16) && scan_tc_supported(p, dtype))
-    return launch_scan_tc(p, units, out_dtype, stream);
-  return launch_scan(p, units, dtype, out_dtype, stream);
+// Whether a call whose results end up in bf16 (or not) runs the tcgen05 form.
+static bool use_tc(const Scan &p, int dtype, int result_dtype) {
+  return result_dtype == GDN_DTYPE_BF16 && scan_tc_supported(p, dtype);
+}
+
+static cudaError_t run_scan(const Scan &p, bool tc, int units, int dtype, int out_dtype, cudaStream_t stream) {
+  return tc ? launch_scan_tc(p, units, out_dtype, stream) : launch_scan(p, units, dtype, out_dtype, stream);
 }
 
 // Plan the segments and point `p` at the tables.
@@ -467,28 +479,30 @@ cudaError_t launch_linear_prefill(const void *q, const void *k, const void *v, c
                                   int dtype, int o_dtype, int state_dtype, float scale, const void *s0,
                                   void *sf, void *o, void *ws, cudaStream_t stream) {
   using namespace lin;
-  const lin::Layout l = layout(N, T, Hqk, Hv, Dk, Dv, false);
   unsigned char *w = static_cast<unsigned char *>(ws);
   Scan p = {};
   p.a = q; p.b = k; p.c = v; p.Ha = p.Hb = Hqk; p.Hc = Hv; p.g = g; p.cu = cu; p.N = N; p.T = (int)T;
-  p.Hv = Hv; p.Da = Dk; p.Dc = Dv; p.s_intra = p.s_inter = scale; p.s_upd = 1.f; p.L = l.L;
+  p.Hv = Hv; p.Da = Dk; p.Dc = Dv; p.s_intra = p.s_inter = scale; p.s_upd = 1.f;
+  const bool tc = use_tc(p, dtype, o_dtype);
+  const lin::Layout l = layout(N, T, Hqk, Hv, Dk, Dv, tc, false);
+  p.L = l.L;
   p.status = static_cast<int32_t *>(ws);
   p.x0 = s0; p.xf = sf; p.x_bf16 = state_dtype == GDN_DTYPE_BF16;
   if (T <= l.L) {
     p.out = o;
-    return run_scan(p, N * Hv, dtype, o_dtype, o_dtype, stream);
+    return run_scan(p, tc, N * Hv, dtype, o_dtype, stream);
   }
   cudaError_t e = run_plan(p, l, w, stream);
   if (e != cudaSuccess) return e;
   p.seg_state = reinterpret_cast<float *>(w + l.nat);
   const int units = (int)l.max_seg * Hv;
-  if ((e = run_scan(p, units, dtype, dtype, dtype, stream)) != cudaSuccess) return e;  // out NULL: states
+  if ((e = run_scan(p, tc, units, dtype, dtype, stream)) != cudaSuccess) return e;  // out NULL: states
   Prefix x = {};
   x.g = g; x.cu = cu; x.first_seg = p.first_seg; x.N = N; x.Hv = Hv; x.L = l.L; x.Da = Dk; x.Dc = Dv;
   x.nat = p.seg_state; x.keep_nat = 1; x.x0 = s0; x.xf = sf; x.x_bf16 = p.x_bf16;
   if ((e = run_prefix(x, stream)) != cudaSuccess) return e;
   p.out = o;
-  return run_scan(p, units, dtype, o_dtype, o_dtype, stream);
+  return run_scan(p, tc, units, dtype, o_dtype, stream);
 }
 
 cudaError_t launch_linear_backward(const void *q, const void *k, const void *v, const float *g,
@@ -497,11 +511,13 @@ cudaError_t launch_linear_backward(const void *q, const void *k, const void *v, 
                                    const float *dsf, void *dq, void *dk, void *dv, float *ds0, void *ws,
                                    cudaStream_t stream) {
   using namespace lin;
-  const lin::Layout l = layout(N, T, Hqk, Hv, Dk, Dv, true);
   unsigned char *w = static_cast<unsigned char *>(ws);
-  const bool one = T <= l.L, grouped = Hv > Hqk;
   Scan base = {};
-  base.g = g; base.cu = cu; base.N = N; base.T = (int)T; base.Hv = Hv; base.L = l.L;
+  base.g = g; base.cu = cu; base.N = N; base.T = (int)T; base.Hv = Hv;
+  const bool tc = use_tc(base, dtype, dtype);
+  const lin::Layout l = layout(N, T, Hqk, Hv, Dk, Dv, tc, true);
+  base.L = l.L;
+  const bool one = T <= l.L, grouped = Hv > Hqk;
   base.status = static_cast<int32_t *>(ws);
   float *nat = reinterpret_cast<float *>(w + l.nat), *tr = reinterpret_cast<float *>(w + l.tr);
   float *part = reinterpret_cast<float *>(w + l.part);
@@ -515,7 +531,7 @@ cudaError_t launch_linear_backward(const void *q, const void *k, const void *v, 
   // dq (and dk) of a query/key head: fp32 partials of its value heads, then their sum
   auto into = [&](Scan p, void *out) -> cudaError_t {
     p.out = grouped ? part : out;
-    cudaError_t r = run_scan(p, units, dtype, grouped ? GDN_DTYPE_FP32 : dtype, dtype, stream);
+    cudaError_t r = run_scan(p, tc, units, dtype, grouped ? GDN_DTYPE_FP32 : dtype, stream);
     if (r != cudaSuccess || !grouped) return r;
     const size_t quads = (size_t)T * Hqk * Dk / 4;
     const unsigned blocks = (unsigned)((quads + 255) / 256);
@@ -530,7 +546,7 @@ cudaError_t launch_linear_backward(const void *q, const void *k, const void *v, 
   p.a = q; p.Ha = Hqk; p.b = k; p.Hb = Hqk; p.c = v; p.Hc = Hv; p.Da = Dk; p.Dc = Dv; p.s_upd = 1.f;
   if (!one) {
     p.seg_state = nat;
-    if ((e = run_scan(p, units, dtype, dtype, dtype, stream)) != cudaSuccess) return e;
+    if ((e = run_scan(p, tc, units, dtype, dtype, stream)) != cudaSuccess) return e;
     x.x0 = s0; x.back = 0; x.keep_nat = 0;
     if ((e = run_prefix(x, stream)) != cudaSuccess) return e;
   }
@@ -544,12 +560,12 @@ cudaError_t launch_linear_backward(const void *q, const void *k, const void *v, 
   p.a = k; p.Ha = Hqk; p.b = q; p.Hb = Hqk; p.c = d_o; p.Hc = Hv; p.Da = Dk; p.Dc = Dv;
   p.s_intra = p.s_upd = scale; p.s_inter = 1.f; p.seg_state = nat; p.x0 = dsf; p.xf = ds0;
   if (!one) {
-    if ((e = run_scan(p, units, dtype, dtype, dtype, stream)) != cudaSuccess) return e;
+    if ((e = run_scan(p, tc, units, dtype, dtype, stream)) != cudaSuccess) return e;
     x.x0 = dsf; x.back = 1; x.keep_nat = 1; x.xf = ds0;
     if ((e = run_prefix(x, stream)) != cudaSuccess) return e;
   }
   p.out = dv;
-  if ((e = run_scan(p, units, dtype, dtype, dtype, stream)) != cudaSuccess) return e;
+  if ((e = run_scan(p, tc, units, dtype, dtype, stream)) != cudaSuccess) return e;
   p.a = v; p.Ha = Hv; p.b = d_o; p.Hb = Hv; p.c = q; p.Hc = Hqk; p.Da = Dv; p.Dc = Dk;
   p.seg_state = tr; p.x0_tr = 1; p.xf = nullptr;
   return into(p, dk);

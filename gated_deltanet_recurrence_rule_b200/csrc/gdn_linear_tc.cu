@@ -1,6 +1,6 @@
 // gdn_linear_tc.cu -- the scan of linear attention (gdn_linear.cuh) on the
 // Blackwell tensor cores: tcgen05 with TMEM accumulators, TMA tiles; bf16 operands
-// and output, head dims 128, fp32 state.
+// and output, head dims 128 or 64, fp32 state.
 //
 // Chunks of 128 tokens, so that every product is a full 128 x 128 x 128 tile:
 //     P  = A B^T                     A, B, C: the chunk's rows of a, b, c
@@ -8,6 +8,10 @@
 //     Oa = (P . lam^{|t-s|}) C       causal
 //     dX = (w C)^T B                 w_t = s_upd lam^{rest}
 //     out_t = s_inter lam^{p+1} Oi_t + s_intra Oa_t,   X <- lam^len X + dX.
+// A head dim of 64 runs on the same tiles: TMA fills the columns past it with zeros and
+// does not store them.  (The products are then up to four times what is needed, but
+// the loads, stores and elementwise work bound the kernel: 8192 tokens at 16/48 heads
+// take as long as the halved bytes allow less about a tenth.)
 // Precision.  A, B, C are exact bf16.  The state is fp32 in registers; w C enters dX
 // as bf16 terms cut from its fp32 value, 8 bits each: three (all 24 bits) where the
 // state is returned or handed to another segment, two where it only serves outputs;
@@ -31,7 +35,7 @@ using chunk::CTL_LIMIT;
 
 namespace {
 
-constexpr int CH = 128, HD = 128;
+constexpr int CH = 128;
 constexpr int NTHREADS = 640;   // states: warp 0 TMA, 1 MMA, 2 wait limit, 4-19 elementwise
 constexpr int NTHREADS_O = 1024;  // outputs: warp 0 loads, 1 and 3 MMA, 2 stores, 4-7 w C, 8-15 X, 16-23 P, 24-31 out
 constexpr uint32_t TILE = 32768;  // 128 rows x 128 bf16: [d 0-63 | d 64-127], 128-byte rows, swizzled
@@ -397,7 +401,7 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
 #pragma unroll 1
           for (int i = 0; i < 8; ++i) {
             const int hf = i >> 2, r = 32 * (i & 3);
-            if (r + 32 <= len)
+            if (r + 32 <= len && 64 * hf < p.Dc)
               tma_store_3d(&tm_o, sb + s * STAGE + hf * 16384 + r * 128, 64 * hf + j * 32, u.h, u.t0 + c * CH + r);
           }
           bulk_commit_group();
@@ -448,7 +452,10 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     const int lq = warp & 3, row = 32 * lq + lane;  // TMEM lane: row of X and dX
     const uint32_t tl = tmem + ((uint32_t)(32 * lq) << 16);
     float X[64];
-    load_start<64>(p, u, gh, row, 64 * hf, X);
+    if (row < p.Dc && 64 * hf < p.Da) load_start<64>(p, u, row, 64 * hf, X);
+    else
+#pragma unroll
+      for (int i = 0; i < 64; ++i) X[i] = 0.f;
     auto put_x = [&]() {
       unsigned char *xo = smem + OFF_X + hf * 16384;
 #pragma unroll
@@ -483,9 +490,9 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         put_x();
       }
     }
-    if (ok && exact) {
+    if (ok && exact && row < p.Dc && 64 * hf < p.Da) {
       const float f = BACK && nch > 0 ? expf(gh) : 1.f;
-      const size_t e0 = (((size_t)u.n * p.Hv + u.h) * HD + row) * HD + 64 * hf;
+      const size_t e0 = (((size_t)u.n * p.Hv + u.h) * p.Dc + row) * p.Da + 64 * hf;
 #pragma unroll
       for (int i = 0; i < 64; i += 4) {
         const float y[4] = {f * X[i], f * X[i + 1], f * X[i + 2], f * X[i + 3]};
@@ -595,8 +602,8 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             for (int k = 0; k < W; k += 4)
               *reinterpret_cast<uint4 *>(box + sw128_off(lane, i * (int)sizeof(TO) / 16 + k / 4)) =
                   make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
-          } else if (row < len) {  // the rows after belong to the next sequence
-            TO *o = static_cast<TO *>(p.out) + ((size_t)(u.t0 + c * CH + row) * p.Hv + u.h) * HD + 64 * hf + j + i;
+          } else if (row < len && 64 * hf < p.Dc) {  // the rows after belong to the next sequence
+            TO *o = static_cast<TO *>(p.out) + ((size_t)(u.t0 + c * CH + row) * p.Hv + u.h) * p.Dc + 64 * hf + j + i;
 #pragma unroll
             for (int k = 0; k < W; k += 4)
               *reinterpret_cast<uint4 *>(o + k * 4 / (int)sizeof(TO)) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
@@ -761,8 +768,8 @@ scan_state_tc_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_cons
 #pragma unroll
       for (int i = 0; i < 32; ++i) X[i] = fmaf(lx, X[i], d[i]);
     }
-    if (ok) {
-      float *x = p.seg_state + (((size_t)u.seg * p.Hv + u.h) * HD + row) * HD + 32 * q;
+    if (ok && row < p.Dc && 32 * q < p.Da) {
+      float *x = p.seg_state + (((size_t)u.seg * p.Hv + u.h) * p.Dc + row) * p.Da + 32 * q;
 #pragma unroll
       for (int i = 0; i < 32; i += 4)
         *reinterpret_cast<float4 *>(x + i) = make_float4(X[i], X[i + 1], X[i + 2], X[i + 3]);
@@ -776,10 +783,10 @@ scan_state_tc_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_cons
   }
 }
 
-// Tensor map of a packed [T, H, 128] bf16 (or fp32) tensor viewed as (d, head, token),
-// box 128 bytes of d x 1 head x `rows` tokens, 128-byte swizzle.  Tokens past T read as
-// zeros.
-bool make_map(CUtensorMap *m, const void *base, int H, int T, bool fp32 = false, int rows = CH) {
+// Tensor map of a packed [T, H, D] bf16 (or fp32) tensor viewed as (d, head, token), box
+// 128 bytes of d x 1 head x `rows` tokens, 128-byte swizzle.  Tokens past T and columns
+// past D read as zeros and are not written.
+bool make_map(CUtensorMap *m, const void *base, int H, int T, int D, bool fp32 = false, int rows = CH) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     void *fn = nullptr;
     cudaDriverEntryPointQueryResult res;
@@ -789,9 +796,9 @@ bool make_map(CUtensorMap *m, const void *base, int H, int T, bool fp32 = false,
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }();
   if (!encode) return false;
-  const cuuint64_t dims[3] = {HD, (cuuint64_t)H, (cuuint64_t)T};
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
   const cuuint64_t eb = fp32 ? 4 : 2;
-  const cuuint64_t strides[2] = {HD * eb, (cuuint64_t)H * HD * eb};
+  const cuuint64_t strides[2] = {D * eb, (cuuint64_t)H * D * eb};
   const cuuint32_t box[3] = {fp32 ? 32u : 64u, 1, (cuuint32_t)rows}, elem[3] = {1, 1, 1};
   return encode(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, elem,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -801,21 +808,20 @@ bool make_map(CUtensorMap *m, const void *base, int H, int T, bool fp32 = false,
 }  // namespace
 
 bool scan_tc_supported(const Scan &p, int dtype) {
-  return p.Da == HD && p.Dc == HD && dtype == GDN_DTYPE_BF16 && p.T > 0 &&
-         p.T <= INT32_MAX - CH;
+  return dtype == GDN_DTYPE_BF16 && p.T > 0 && p.T <= INT32_MAX - CH;
 }
 
 cudaError_t launch_scan_tc(const Scan &p, int units, int out_dtype, cudaStream_t stream) {
   static std::atomic<bool> f0[64], f1[64], f2[64], f3[64], f4[64];
   CUtensorMap ma, mb, mc, mo;
-  if (!make_map(&mb, p.b, p.Hb, p.T) || !make_map(&mc, p.c, p.Hc, p.T)) return cudaErrorInvalidValue;
+  if (!make_map(&mb, p.b, p.Hb, p.T, p.Da) || !make_map(&mc, p.c, p.Hc, p.T, p.Dc)) return cudaErrorInvalidValue;
   cudaError_t e;
   if (!p.out) {
     if ((e = set_smem_once(scan_state_tc_kernel, SMEM_STATE, f0)) != cudaSuccess) return e;
     scan_state_tc_kernel<<<(unsigned)units, NTHREADS, SMEM_STATE, stream>>>(mb, mc, p);
     return cudaGetLastError();
   }
-  if (!make_map(&ma, p.a, p.Ha, p.T) || !make_map(&mo, p.out, p.Hv, p.T, out_dtype == GDN_DTYPE_FP32, 32))
+  if (!make_map(&ma, p.a, p.Ha, p.T, p.Da) || !make_map(&mo, p.out, p.Hv, p.T, p.Dc, out_dtype == GDN_DTYPE_FP32, 32))
     return cudaErrorInvalidValue;
   auto go = [&](auto kern, std::atomic<bool>(&flags)[64]) {
     const cudaError_t r = set_smem_once(kern, SMEM_OUT, flags);

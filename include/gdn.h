@@ -445,7 +445,7 @@ size_t gdn_linear_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens,
  * 256-byte aligned, zero-filled once; its first word is the sticky status word
  * (gdn_get_device_status), its second the limit of bounded waits, as there.
  *
- * bf16 inputs and bf16 o at head dim 128 run on the tensor cores (tcgen05), with
+ * bf16 inputs with bf16 o run on the tensor cores (tcgen05), with
  * the state in fp32 and its increments from products exact to fp32; the state and
  * the token x token products are rounded to bf16 once, as operands of o, which is
  * itself rounded to bf16.  Everything else runs on warp-level tf32 MMAs with split
