@@ -38,10 +38,8 @@ struct Scan {
   int N, T, Hv, Da, Dc;
   int back;
   float s_intra, s_inter, s_upd;
-  // segments: plan tables, NULL where each sequence is one segment
-  const int32_t *first_seg;  // [N + 1] first segment of each sequence; < 0 at N: bad cu_seqlens
-  const int32_t *seg_seq;    // [segments] sequence of each segment
-  const int32_t *order;      // [segments] the order they are worked on, longest first
+  const int4 *units;         // [segments] the segments, longest first (below); NULL where each
+                             // sequence is one segment
   int L;
   float *seg_state;          // [segments, Hv, Dc, Da] added (states only) or starting state;
                              // a sequence of one segment starts from x0 (and x0 may be xf: of
@@ -58,20 +56,24 @@ struct Unit {
   int first, last;  // the segment its sequence's scan starts, ends with
 };
 
+// A segment of the plan: x its number, with kFirst and kLast where it is the first or
+// last of its sequence (-1: no segment), y the sequence, z and w its tokens.
+constexpr int kFirst = 1 << 30, kLast = 1 << 29;
+
 // False where unit `u` does not exist or cu_seqlens is inconsistent.
 __device__ __forceinline__ bool get_unit(const Scan &p, int u, Unit &w) {
   w.seg = u / p.Hv;
   w.h = u - w.seg * p.Hv;
-  if (p.first_seg) {
-    if (w.seg >= p.first_seg[p.N]) return false;
-    w.seg = p.order[w.seg];
-    w.n = p.seg_seq[w.seg];
-    const int i = w.seg - p.first_seg[w.n], cnt = p.first_seg[w.n + 1] - p.first_seg[w.n];
-    const int c1 = p.cu[w.n + 1];
-    w.t0 = p.cu[w.n] + i * p.L;
-    w.t1 = min(w.t0 + p.L, c1);
-    w.first = i == (p.back ? cnt - 1 : 0);
-    w.last = i == (p.back ? 0 : cnt - 1);
+  if (p.units) {
+    const int4 s = p.units[w.seg];
+    if (s.x < 0) return false;
+    w.seg = s.x & (kLast - 1);
+    w.n = s.y;
+    w.t0 = s.z;
+    w.t1 = s.w;
+    const int first = (s.x & kFirst) != 0, last = (s.x & kLast) != 0;
+    w.first = p.back ? last : first;
+    w.last = p.back ? first : last;
     return true;
   }
   w.n = w.seg;
@@ -102,23 +104,6 @@ __device__ __forceinline__ float initial_state(const Scan &p, const Unit &w, int
 __device__ __forceinline__ float start_state(const Scan &p, const Unit &w, int i, int j) {
   if (!w.first || !w.last) return p.seg_state[(((size_t)w.seg * p.Hv + w.h) * p.Dc + i) * p.Da + j];
   return initial_state(p, w, i, j);
-}
-
-// W consecutive elements of row i of it (j a multiple of 4).
-template <int W>
-__device__ __forceinline__ void load_start(const Scan &p, const Unit &w, int i, int j, float *x) {
-  if (!w.first || !w.last) {
-    const float *s = p.seg_state + (((size_t)w.seg * p.Hv + w.h) * p.Dc + i) * p.Da + j;
-#pragma unroll
-    for (int k = 0; k < W; k += 4) load4(s + k, x + k);
-  } else if (p.x0 && !p.x0_tr) {
-    const size_t e = (((size_t)w.n * p.Hv + w.h) * p.Dc + i) * p.Da + j;
-#pragma unroll
-    for (int k = 0; k < W; k += 4) load_state4(p.x0, e + k, p.x_bf16, x + k);
-  } else {
-#pragma unroll
-    for (int k = 0; k < W; ++k) x[k] = initial_state(p, w, i, j + k);
-  }
 }
 
 // ---- host ----

@@ -15,15 +15,17 @@ using chunk::mma_tf32_16x8x8;
 using chunk::to_tf32;
 
 // ---------------------------------------------------------------- plan
-// Segment tables of the packed sequences, by one CTA.  Units of unequal length are
-// started longest first, so that the last ones to finish are short; beyond
-// kMaxSorted segments there are enough waves of units for the order not to matter.
+// The segments of the packed sequences (an empty one has one, of no tokens), by one
+// CTA.  Units of unequal length are started longest first, so that the last ones to
+// finish are short; beyond kMaxSorted segments there are enough waves of units for the
+// order not to matter.  Entries past the last segment, and all of them where cu_seqlens
+// is inconsistent, are marked.
 constexpr int kMaxSorted = 512;
 __global__ void __launch_bounds__(1024)
-plan_segments_kernel(const int32_t *__restrict__ cu, int N, int T, int L, int32_t *first_seg,
-                     int32_t *seg_seq, int32_t *order, int32_t *status) {
+plan_segments_kernel(const int32_t *__restrict__ cu, int N, int T, int L, int max_seg, int32_t *first_seg,
+                     int4 *units, int32_t *status) {
   __shared__ int wsum[32], run_s;
-  __shared__ int length[kMaxSorted];
+  __shared__ int4 table[kMaxSorted];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   int bad = 0;
   for (int i = tid; i <= N; i += 1024) {
@@ -36,11 +38,13 @@ plan_segments_kernel(const int32_t *__restrict__ cu, int N, int T, int L, int32_
       report_status(status, GDN_ERR_BAD_SEQLENS);
       first_seg[N] = -1;
     }
+    for (int i = tid; i < max_seg; i += 1024) units[i].x = -1;
     return;
   }
   for (int base = 0; base < N; base += 1024) {
     const int n = base + tid;
-    const int cnt = n < N ? (cu[n + 1] - cu[n] + L - 1) / L : 0;
+    const int c0 = n < N ? cu[n] : 0, c1 = n < N ? cu[n + 1] : 0;
+    const int cnt = n < N ? max(1, (int)(((long long)c1 - c0 + L - 1) / L)) : 0;
     int inc = cnt;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -63,9 +67,11 @@ plan_segments_kernel(const int32_t *__restrict__ cu, int N, int T, int L, int32_
     if (n < N) {
       first_seg[n] = start;
       for (int i = 0; i < cnt; ++i) {
-        seg_seq[start + i] = n;
-        order[start + i] = start + i;
-        if (start + i < kMaxSorted) length[start + i] = min(L, cu[n + 1] - cu[n] - i * L);
+        const int sg = start + i;
+        const int4 s = make_int4(sg | (i == 0 ? kFirst : 0) | (i == cnt - 1 ? kLast : 0), n, c0 + i * L,
+                                 i == cnt - 1 ? c1 : c0 + (i + 1) * L);
+        units[sg] = s;
+        if (sg < kMaxSorted) table[sg] = s;
       }
     }
     __syncthreads();
@@ -74,16 +80,23 @@ plan_segments_kernel(const int32_t *__restrict__ cu, int N, int T, int L, int32_
   }
   const int total = run_s;
   if (tid == 0) first_seg[N] = total;
+  for (int i = total + tid; i < max_seg; i += 1024) units[i].x = -1;
   if (total <= kMaxSorted && tid < total) {
+    const int len = table[tid].w - table[tid].z;
     int rank = 0;
-    for (int i = 0; i < total; ++i) rank += length[i] > length[tid] || (length[i] == length[tid] && i < tid);
-    order[rank] = tid;
+    for (int i = 0; i < total; ++i) {
+      const int other = table[i].w - table[i].z;
+      rank += other > len || (other == len && i < tid);
+    }
+    units[rank] = table[tid];
   }
 }
 
 // ---------------------------------------------------------------- prefix
 // Per (sequence of several segments, head): the states that the segments add become
-// the states that they start from, in place (`nat`) and/or transposed (`tr`).  One CTA per 32 x 32 tile of one state: 4 elements a thread.
+// the states that they start from, in place (`nat`) and/or transposed (`tr`), and what
+// follows the last is the final state.  One CTA per 32 x 32 tile of one state: 4
+// elements a thread, four segments' loads in flight.
 struct Prefix {
   const float *g;
   const int32_t *cu, *first_seg;
@@ -91,49 +104,57 @@ struct Prefix {
   float *nat, *tr;
   int keep_nat;      // the starting states are wanted in nat
   const void *x0;    // [N, Hv, Dc, Da]
-  void *xf;          // final states, of empty sequences and of several segments; NULL to skip
+  void *xf;          // final states; NULL to skip
   int x_bf16;
 };
 
 __global__ void __launch_bounds__(256) prefix_kernel(const Prefix p) {
   __shared__ float tile[32][33];
-  if (p.first_seg[p.N] < 0) return;  // inconsistent cu_seqlens
   const int tiles = (p.Da / 32) * (p.Dc / 32);
   const int unit = blockIdx.x / tiles, tl = blockIdx.x - unit * tiles;
   const int n = unit / p.Hv, h = unit - n * p.Hv;
+  const int total = p.first_seg[p.N], s0 = p.first_seg[n], s1 = p.first_seg[n + 1];
+  const int len = p.cu[n + 1] - p.cu[n], cnt = s1 - s0;
+  const float gh = fmaxf(p.g[h], -30.f);
+  if (total < 0 || cnt < 2) return;  // inconsistent cu_seqlens; one segment
   const int i0 = 32 * (tl / (p.Da / 32)), j0 = 32 * (tl % (p.Da / 32));
   const int r = threadIdx.x >> 3, c = 4 * (threadIdx.x & 7);
   const size_t in_state = (size_t)(i0 + r) * p.Da + j0 + c;
   const size_t state = (size_t)p.Da * p.Dc;
-  const int s0 = p.first_seg[n], cnt = p.first_seg[n + 1] - s0;
-  const int len = p.cu[n + 1] - p.cu[n];
-  const float gh = fmaxf(p.g[h], -30.f);
   const size_t e0 = ((size_t)n * p.Hv + h) * state + in_state;
   float x[4] = {0.f, 0.f, 0.f, 0.f};
   if (p.x0) load_state4(p.x0, e0, p.x_bf16, x);
-  if (cnt == 0 && p.xf) store_state4(p.xf, e0, p.x_bf16, x);
-  for (int i = 0; i < cnt && cnt > 1; ++i) {
-    const int sg = p.back ? cnt - 1 - i : i;
-    const size_t at = ((size_t)(s0 + sg) * p.Hv + h) * state;
-    float add[4];
-    const bool go_on = i + 1 < cnt || p.xf;
-    if (go_on) load4(p.nat + at + in_state, add);  // before its place takes the starting state
-    if (p.keep_nat) *reinterpret_cast<float4 *>(p.nat + at + in_state) = make_float4(x[0], x[1], x[2], x[3]);
-    if (p.tr) {
-      __syncthreads();
+  // what the last segment adds is there only where the final state is wanted
+  const int adds = p.xf ? cnt : cnt - 1;
+  for (int b = 0; b < cnt; b += 4) {
+    float add[4][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) tile[c + k][r] = x[k];
-      __syncthreads();
-      *reinterpret_cast<float4 *>(p.tr + at + (size_t)(j0 + r) * p.Dc + i0 + c) =
-          make_float4(tile[r][c], tile[r][c + 1], tile[r][c + 2], tile[r][c + 3]);
+    for (int i = 0; i < 4; ++i) {
+      const int sg = p.back ? cnt - 1 - (b + i) : b + i;
+      if (b + i < adds) load4(p.nat + ((size_t)(s0 + sg) * p.Hv + h) * state + in_state, add[i]);
     }
-    if (!go_on) break;
-    const int tokens = min(p.L, len - sg * p.L) - (p.back && i == 0 ? 1 : 0);
-    const float f = expf(gh * (float)tokens);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = fmaf(f, x[k], add[k]);
+    for (int i = 0; i < 4; ++i) {
+      if (b + i >= cnt) break;
+      const int sg = p.back ? cnt - 1 - (b + i) : b + i;
+      const size_t at = ((size_t)(s0 + sg) * p.Hv + h) * state;
+      if (p.keep_nat) *reinterpret_cast<float4 *>(p.nat + at + in_state) = make_float4(x[0], x[1], x[2], x[3]);
+      if (p.tr) {
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tile[c + k][r] = x[k];
+        __syncthreads();
+        *reinterpret_cast<float4 *>(p.tr + at + (size_t)(j0 + r) * p.Dc + i0 + c) =
+            make_float4(tile[r][c], tile[r][c + 1], tile[r][c + 2], tile[r][c + 3]);
+      }
+      if (b + i >= adds) break;
+      const int tokens = min(p.L, len - sg * p.L) - (p.back && b + i == 0 ? 1 : 0);
+      const float f = expf(gh * (float)tokens);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = fmaf(f, x[k], add[i][k]);
+    }
   }
-  if (cnt > 1 && p.xf) {
+  if (p.xf) {
     const float f = p.back ? expf(gh) : 1.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[k] *= f;
@@ -408,7 +429,7 @@ int segment_len(int64_t T, int Hv, int Dv, bool tc) {
 struct Layout {
   int L;
   int64_t max_seg;
-  size_t first_seg, seg_seq, order, nat, tr, part, total;
+  size_t first_seg, units, nat, tr, part, total;
 };
 
 Layout layout(int64_t N, int64_t T, int Hqk, int Hv, int Dk, int Dv, bool tc, bool backward) {
@@ -419,10 +440,8 @@ Layout layout(int64_t N, int64_t T, int Hqk, int Hv, int Dk, int Dv, bool tc, bo
   size_t at = kWorkspaceHeaderBytes;
   l.first_seg = at;
   if (!one) at = round_up(at + sizeof(int32_t) * (size_t)(N + 1), 256);
-  l.seg_seq = at;
-  if (!one) at = round_up(at + sizeof(int32_t) * (size_t)l.max_seg, 256);
-  l.order = at;
-  if (!one) at = round_up(at + sizeof(int32_t) * (size_t)l.max_seg, 1024);
+  l.units = at;
+  if (!one) at = round_up(at + sizeof(int4) * (size_t)l.max_seg, 1024);
   const size_t states = one ? 0 : round_up((size_t)l.max_seg * Hv * Dk * Dv * sizeof(float), 1024);
   l.nat = at;
   at += states;
@@ -454,15 +473,13 @@ static cudaError_t run_scan(const Scan &p, bool tc, int units, int dtype, int ou
   return tc ? launch_scan_tc(p, units, out_dtype, stream) : launch_scan(p, units, dtype, out_dtype, stream);
 }
 
-// Plan the segments and point `p` at the tables.
-static cudaError_t run_plan(Scan &p, const Layout &l, unsigned char *ws, cudaStream_t stream) {
+// Plan the segments; point `p` at them and `x` at the first of each sequence.
+static cudaError_t run_plan(Scan &p, Prefix &x, const Layout &l, unsigned char *ws, cudaStream_t stream) {
   int32_t *first_seg = reinterpret_cast<int32_t *>(ws + l.first_seg);
-  int32_t *seg_seq = reinterpret_cast<int32_t *>(ws + l.seg_seq);
-  int32_t *order = reinterpret_cast<int32_t *>(ws + l.order);
-  plan_segments_kernel<<<1, 1024, 0, stream>>>(p.cu, p.N, p.T, l.L, first_seg, seg_seq, order, p.status);
-  p.first_seg = first_seg;
-  p.seg_seq = seg_seq;
-  p.order = order;
+  int4 *units = reinterpret_cast<int4 *>(ws + l.units);
+  plan_segments_kernel<<<1, 1024, 0, stream>>>(p.cu, p.N, p.T, l.L, (int)l.max_seg, first_seg, units, p.status);
+  p.units = units;
+  x.first_seg = first_seg;
   return cudaGetLastError();
 }
 
@@ -492,13 +509,13 @@ cudaError_t launch_linear_prefill(const void *q, const void *k, const void *v, c
     p.out = o;
     return run_scan(p, tc, N * Hv, dtype, o_dtype, stream);
   }
-  cudaError_t e = run_plan(p, l, w, stream);
+  Prefix x = {};
+  cudaError_t e = run_plan(p, x, l, w, stream);
   if (e != cudaSuccess) return e;
   p.seg_state = reinterpret_cast<float *>(w + l.nat);
   const int units = (int)l.max_seg * Hv;
   if ((e = run_scan(p, tc, units, dtype, dtype, stream)) != cudaSuccess) return e;  // out NULL: states
-  Prefix x = {};
-  x.g = g; x.cu = cu; x.first_seg = p.first_seg; x.N = N; x.Hv = Hv; x.L = l.L; x.Da = Dk; x.Dc = Dv;
+  x.g = g; x.cu = cu; x.N = N; x.Hv = Hv; x.L = l.L; x.Da = Dk; x.Dc = Dv;
   x.nat = p.seg_state; x.keep_nat = 1; x.x0 = s0; x.xf = sf; x.x_bf16 = p.x_bf16;
   if ((e = run_prefix(x, stream)) != cudaSuccess) return e;
   p.out = o;
@@ -523,9 +540,9 @@ cudaError_t launch_linear_backward(const void *q, const void *k, const void *v, 
   float *part = reinterpret_cast<float *>(w + l.part);
   const int units = (int)l.max_seg * Hv;
   cudaError_t e = cudaSuccess;
-  if (!one && (e = run_plan(base, l, w, stream)) != cudaSuccess) return e;
   Prefix x = {};
-  x.g = g; x.cu = cu; x.first_seg = base.first_seg; x.N = N; x.Hv = Hv; x.L = l.L; x.Da = Dk; x.Dc = Dv;
+  if (!one && (e = run_plan(base, x, l, w, stream)) != cudaSuccess) return e;
+  x.g = g; x.cu = cu; x.N = N; x.Hv = Hv; x.L = l.L; x.Da = Dk; x.Dc = Dv;
   x.nat = nat; x.tr = tr;
 
   // dq (and dk) of a query/key head: fp32 partials of its value heads, then their sum

@@ -107,6 +107,16 @@ __device__ __forceinline__ int wait_limit(const int32_t *status) {
   return us ? (int)(2u * min(us, 0x3fffffffu)) : 4000000;
 }
 
+// 8 consecutive fp32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float *v) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 // One 16-bit term of two fp32 values: their upper halves in one word, and what they
 // leave.  Three such terms hold all 24 bits of a value.
 __device__ __forceinline__ uint32_t cut_term(float &x0, float &x1) {
@@ -183,14 +193,25 @@ __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// A row of a state is 512 bytes and a thread holds a piece of one, so states pass
+// through shared memory, where a piece has a slot of its own with 16 bytes to spare
+// (no bank conflicts), and are copied piece by piece.  (Rows of 32 scattered pieces
+// loaded and stored directly took 4 us of a CTA each.)
+__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)),
+               "r"(src), "r"(bytes)
+               : "memory");
+}
+
 // ---------------------------------------------------------------- outputs
 // Shared memory of the output kernel: 2 stages of A, B, C tiles, X as an operand.
 constexpr uint32_t STAGE = 3 * TILE;
 constexpr uint32_t OFF_X = 2 * STAGE;
 constexpr uint32_t OFF_W = OFF_X + TILE;
 constexpr uint32_t OFF_BAR = OFF_W + ((sizeof(Weights) + 15) / 16) * 16;
-constexpr uint32_t OFF_CTL = OFF_BAR + 192;  // TMEM base, control words
-constexpr uint32_t SMEM_OUT = OFF_CTL + 32;
+constexpr uint32_t OFF_CTL = OFF_BAR + 240;  // TMEM base, control words
+constexpr uint32_t OFF_UNIT = OFF_CTL + 32;  // the unit, for the end of the X warps
+constexpr uint32_t SMEM_OUT = OFF_UNIT + 32;
 static_assert(SMEM_OUT <= 232448, "shared memory of a CTA");
 
 // TMEM columns: P (fp32), whose two halves are overwritten by their bf16 form (32
@@ -200,16 +221,16 @@ constexpr uint32_t R_P = 0, T_PB = 0, R_O = 128, T_VH = 256, T_VM = 320, R_DX = 
 __host__ __device__ constexpr uint32_t pcol(int kk) { return 64 * (kk >> 2) + 8 * (kk & 3); }  // of T_PB
 
 enum { B_FULL = 0, B_EMPTY = 2, B_P = 4, B_PB = 6, B_V = 7, B_VFREE = 9, B_DX = 11, B_DXFREE = 12, B_OI = 13,
-       B_OA = 14, B_OFREE = 15, B_X = 16, B_FIX = 17, B_DRAIN = 18, B_EMPTYA = 19, B_OUT = 21, B_OUTFREE = 22, NBAR = 23 };
-static_assert(NBAR * 8 <= 192, "barrier area");
+       B_OA = 14, B_OFREE = 15, B_X = 16, B_FIX = 17, B_DRAIN = 18, B_EMPTYA = 19, B_OUT = 21, B_OUTFREE = 22, B_X0 = 23, B_VL = 25, B_VUSED = 27, NBAR = 29 };
+static_assert(NBAR * 8 <= 240, "barrier area");
 
 // One CTA per (segment, head).  Only X <- lam^len X + dX is carried from chunk to
 // chunk; dX, P and the rest of a chunk do not wait for the one before, except for the
 // buffers.  So each kind of work has its own warps, which run as far ahead as the
 // buffers let them:
-//   warps 4-7    w C as bf16 terms, in two halves of 64 tokens with a buffer each; a
-//                third term goes into the first one's buffer when that has been used
-//   warps 8-15   X: adds dX, writes X as an operand
+//   warps 4-7    w C as two bf16 terms, in two halves of 64 tokens with a buffer each
+//   warps 8-15   X: adds dX, writes X as an operand; where a third term of w C is
+//                wanted, writes it into a half's buffer when the first two have been used
 //   warps 16-23  P to its causal bf16 form
 //   warps 24-31  scale A X^T in place (the product with P then adds to it), and put the
 //                outputs where the chunk's A tile was
@@ -221,6 +242,12 @@ __global__ void __launch_bounds__(NTHREADS_O, 1)
 scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                    const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_o, const Scan p) {
   extern __shared__ __align__(1024) unsigned char smem[];
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&tm_a);
+    prefetch_tensormap(&tm_b);
+    prefetch_tensormap(&tm_c);
+    prefetch_tensormap(&tm_o);
+  }
   Unit u;
   if (!get_unit(p, blockIdx.x, u)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -237,14 +264,15 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
   if (tid == 0) {
     for (int i = 0; i < NBAR; ++i) {
       // one arrival per warp of the group that signals; a stage is freed by both issuers
-      const bool eight = i == B_DXFREE || i == B_OFREE || i == B_X || i == B_OUT;
-      const bool four = i == B_V || i == B_V + 1 || i == B_FIX;
+      const bool eight = i == B_DXFREE || i == B_OFREE || i == B_X || i == B_OUT || i == B_X0 || i == B_X0 + 1;
+      const bool four = i == B_V || i == B_V + 1 || i == B_VL || i == B_VL + 1 || i == B_FIX;
       const bool two = i == B_EMPTY || i == B_EMPTY + 1 || i == B_DRAIN;
       mbar_init(bar(i), i == B_PB ? 16 : eight ? 8 : four ? 4 : two ? 2 : 1);
     }
     ctl[CTL_ABORT] = 0;
     ctl[CTL_LIMIT] = 4000000;  // until warp 2 has read the header
     fence_barrier_init();
+    *reinterpret_cast<Unit *>(smem + OFF_UNIT) = u;
   }
   const float gh = head_decay(p, u.h);
   fill_weights(p, wts, gh, tail, tid);
@@ -286,6 +314,8 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         const int s = ci & 1, t = u.t0 + chunk_of(ci) * CH;
         if (ci >= 2) prefetch(ci + 2);
         if (!wait_phase_alone(bar(B_EMPTY + s), ((ci >> 1) & 1) ^ 1, ctl)) break;
+        // (the second stage holds the starting state at first)
+        if (ci == 1 && !wait_phase_alone(bar(B_X0 + 1), 0, ctl)) break;
         const uint32_t st = sb + s * STAGE, fb = bar(B_FULL + s);
         mbar_arrive_expect_tx(fb, STAGE);
         for (int half = 0; half < 2; ++half) {
@@ -361,7 +391,7 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
       for (int j = 0; j < parts; ++j) {  // halves of the tokens; again for the third term
         const int hf = j & 1;
         // (the terms are written after a short tile was zeroed)
-        if (!(ok = warp_wait(B_V + hf, (parts / 2 * ci + (j >> 1)) & 1))) break;
+        if (!(ok = warp_wait(j < 2 ? B_V + hf : B_VL + hf, ph))) break;
         if (elect_one()) {
 #pragma unroll 1
           for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk) {
@@ -369,7 +399,7 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
             mma_bf16_ts(tmem + R_DX, tmem + T_VH + 8 * kk, db, IDESC_KM, j + kk > 0);
             if (j < 2) mma_bf16_ts(tmem + R_DX, tmem + T_VM + 8 * kk, db, IDESC_KM, 1);
           }
-          mma_commit(bar(B_VFREE + hf));
+          mma_commit(bar((j + 2 < parts ? B_VUSED : B_VFREE) + hf));  // used by two terms; by all
           if (j == parts - 1) {
             mma_commit(bar(B_DX));
             mma_commit(bar(B_EMPTY + s));
@@ -433,12 +463,9 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
       const uint32_t ct = sb + s * STAGE + 2 * TILE;
       bool ok = true;
 #pragma unroll 1
-      for (int j = 0; j < parts; ++j) {
-        const int hf = j & 1, n = parts / 2 * ci + (j >> 1);  // n: uses of the buffer before
-        if (n > 0 && !(ok = warp_wait(B_VFREE + hf, (n - 1) & 1))) break;
-        const uint32_t hi = tl + T_VH + 32 * hf, mid = tl + T_VM + 32 * hf;
-        if (j < 2) scale_split<2, 4>(ct, wt, lq, lane, 64 * hf, hi, mid, 0);
-        else scale_split<1, 4>(ct, wt, lq, lane, 64 * hf, hi, 0, 0);
+      for (int hf = 0; hf < 2; ++hf) {
+        if (ci > 0 && !(ok = warp_wait(B_VFREE + hf, (ci - 1) & 1))) break;
+        scale_split<2, 4>(ct, wt, lq, lane, 64 * hf, tl + T_VH + 32 * hf, tl + T_VM + 32 * hf, 0);
         tmem_wait_st();
         tc_fence_before();
         arrive(B_V + hf);
@@ -452,10 +479,39 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     const int lq = warp & 3, row = 32 * lq + lane;  // TMEM lane: row of X and dX
     const uint32_t tl = tmem + ((uint32_t)(32 * lq) << 16);
     float X[64];
-    if (row < p.Dc && 64 * hf < p.Da) load_start<64>(p, u, row, 64 * hf, X);
-    else
 #pragma unroll
-      for (int i = 0; i < 64; ++i) X[i] = 0.f;
+    for (int i = 0; i < 64; ++i) X[i] = 0.f;
+    // (a warp's lanes agree on all of these)
+    const bool mine = row < p.Dc && 64 * hf < p.Da, own = u.first && u.last;  // own: starts from x0
+    const bool some = mine && (!own || p.x0), by_copy = some && !(own && p.x0_tr), bf = own && p.x_bf16 && by_copy;
+    const uint32_t slot = (128 * hf + row) * 272;
+    if (by_copy) {
+      const size_t e0 = (((size_t)(own ? u.n : u.seg) * p.Hv + u.h) * p.Dc + row) * p.Da + 64 * hf;
+      const unsigned char *src = static_cast<const unsigned char *>(own ? p.x0 : p.seg_state) + e0 * (bf ? 2 : 4);
+      const uint32_t bytes = bf ? 128 : 256;
+      if (lane == 0) mbar_arrive_expect_tx(bar(B_X0), 32 * bytes);
+      __syncwarp();
+      bulk_load(sb + STAGE + slot, src, bytes, bar(B_X0));
+    } else {
+      if (some) {
+#pragma unroll 4
+        for (int i = 0; i < 64; ++i)
+          *reinterpret_cast<float *>(smem + STAGE + slot + 4 * i) = initial_state(p, u, row, 64 * hf + i);
+      }
+      arrive(B_X0);
+    }
+    bool ok = warp_wait(B_X0, 0);
+    if (ok && some) {
+      const unsigned char *at = smem + STAGE + slot;
+      if (bf) {
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) load4(reinterpret_cast<const __nv_bfloat16 *>(at) + i, X + i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) load4(reinterpret_cast<const float *>(at) + i, X + i);
+      }
+    }
+    arrive(B_X0 + 1);
     auto put_x = [&]() {
       unsigned char *xo = smem + OFF_X + hf * 16384;
 #pragma unroll
@@ -469,19 +525,30 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
       arrive(B_X);
     };
     if (nch > 0) put_x();
-    bool ok = true;
-    for (int ci = 0; ci < nch; ++ci) {
+    for (int ci = 0; ok && ci < nch; ++ci) {
       const uint32_t ph = ci & 1;
       const int len = chunk_of(ci) == nch - 1 ? tail : CH, skip = BACK && u.first && ci == 0 ? 1 : 0;
+      if (exact) {
+        const int s = ci & 1;
+        const bool last = chunk_of(ci) == nch - 1;
+        if (!(ok = warp_wait(B_FULL + s, (ci >> 1) & 1) && (!last || tail == CH || warp_wait(B_FIX, 0)) &&
+                   warp_wait(B_VUSED + hf, ph)))
+          break;
+        scale_split<1, 4>(sb + s * STAGE + 2 * TILE, last ? wts->wtail : wts->wfull, lq, lane, 64 * hf,
+                          tl + T_VH + 32 * hf, 0, 0);
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(B_VL + hf);
+      }
       if (!(ok = warp_wait(B_DX, ph))) break;
       const float lx = wts->pw[len - skip];
 #pragma unroll
-      for (int i = 0; i < 64; i += 16) {
-        float d[16];
-        tmem_ld16(tl + R_DX + 64 * hf + i, d);
+      for (int i = 0; i < 64; i += 8) {
+        float d[8];
+        tmem_ld8(tl + R_DX + 64 * hf + i, d);
         tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 16; ++k) X[i + k] = fmaf(lx, X[i + k], d[k]);
+        for (int k = 0; k < 8; ++k) X[i + k] = fmaf(lx, X[i + k], d[k]);
       }
       tc_fence_before();
       arrive(B_DXFREE);
@@ -490,13 +557,29 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         put_x();
       }
     }
-    if (ok && exact && row < p.Dc && 64 * hf < p.Da) {
-      const float f = BACK && nch > 0 ? expf(gh) : 1.f;
-      const size_t e0 = (((size_t)u.n * p.Hv + u.h) * p.Dc + row) * p.Da + 64 * hf;
+    if (exact && ok && nch > 1) {  // the stage before the last one, once all have left it
+      const int s = nch & 1;
+      ok = warp_wait(B_EMPTY + s, ((nch - 2) >> 1) & 1) && warp_wait(B_EMPTYA + s, ((nch - 2) >> 1) & 1);
+    }
+    if (exact && ok) {
+      // what only the end needs is read again, not kept through the loop beside X
+      uint32_t t2;
+      asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t2));
+      const volatile Unit *u2 = reinterpret_cast<const volatile Unit *>(smem + OFF_UNIT);
+      const int half = (t2 - 256) >> 7, r = t2 & 127;
+      if (r < p.Dc && 64 * half < p.Da) {
+        const float f = BACK && nch > 0 ? wts->pw[1] : 1.f;
+        const size_t e0 = (((size_t)u2->n * p.Hv + u2->h) * p.Dc + r) * p.Da + 64 * half;
+        const uint32_t at = (nch & 1) * STAGE + (128 * half + r) * 272;
 #pragma unroll
-      for (int i = 0; i < 64; i += 4) {
-        const float y[4] = {f * X[i], f * X[i + 1], f * X[i + 2], f * X[i + 3]};
-        store_state4(p.xf, e0 + i, p.x_bf16, y);
+        for (int i = 0; i < 64; i += 4) {
+          const float y[4] = {f * X[i], f * X[i + 1], f * X[i + 2], f * X[i + 3]};
+          store_state4(smem + at, i, p.x_bf16, y);
+        }
+        fence_proxy_async_smem();
+        bulk_store(static_cast<unsigned char *>(p.xf) + e0 * (p.x_bf16 ? 2 : 4), sb + at, p.x_bf16 ? 128 : 256);
+        bulk_commit_group();
+        bulk_wait_all();
       }
     }
   } else if (warp >= 16 && warp < 24) {
@@ -640,6 +723,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 scan_state_tc_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_c,
                      const Scan p) {
   extern __shared__ __align__(1024) unsigned char smem[];
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&tm_b);
+    prefetch_tensormap(&tm_c);
+  }
   Unit u;
   if (!get_unit(p, blockIdx.x, u)) return;
   if (u.last && (u.first || !p.xf)) return;  // nothing starts from its end
@@ -768,11 +855,15 @@ scan_state_tc_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_cons
 #pragma unroll
       for (int i = 0; i < 32; ++i) X[i] = fmaf(lx, X[i], d[i]);
     }
-    if (ok && row < p.Dc && 32 * q < p.Da) {
-      float *x = p.seg_state + (((size_t)u.seg * p.Hv + u.h) * p.Dc + row) * p.Da + 32 * q;
+    if (ok && row < p.Dc && 32 * q < p.Da) {  // (every tile has been used)
+      const uint32_t at = (128 * q + row) * 144;
 #pragma unroll
       for (int i = 0; i < 32; i += 4)
-        *reinterpret_cast<float4 *>(x + i) = make_float4(X[i], X[i + 1], X[i + 2], X[i + 3]);
+        *reinterpret_cast<float4 *>(smem + at + 4 * i) = make_float4(X[i], X[i + 1], X[i + 2], X[i + 3]);
+      fence_proxy_async_smem();
+      bulk_store(p.seg_state + (((size_t)u.seg * p.Hv + u.h) * p.Dc + row) * p.Da + 32 * q, sb + at, 128);
+      bulk_commit_group();
+      bulk_wait_all();
     }
   }
   tc_fence_before();
