@@ -26,6 +26,8 @@ plan_segments_kernel(const int32_t *__restrict__ cu, int N, int T, int L, int ma
                      int4 *units, int32_t *status) {
   __shared__ int wsum[32], run_s;
   __shared__ int4 table[kMaxSorted];
+  pdl_wait();  // nothing is read before the previous kernel on the stream is done
+  pdl_allow_next();
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   int bad = 0;
   for (int i = tid; i <= N; i += 1024) {
@@ -110,6 +112,8 @@ struct Prefix {
 
 __global__ void __launch_bounds__(256) prefix_kernel(const Prefix p) {
   __shared__ float tile[32][33];
+  pdl_wait();  // nothing is read before the previous kernel on the stream is done
+  pdl_allow_next();
   const int tiles = (p.Da / 32) * (p.Dc / 32);
   const int unit = blockIdx.x / tiles, tl = blockIdx.x - unit * tiles;
   const int n = unit / p.Hv, h = unit - n * p.Hv;
@@ -202,6 +206,8 @@ __global__ void __launch_bounds__(256) scan_kernel(const Scan p) {
   constexpr bool EX = sizeof(T) == 2;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem<DA> &s = *reinterpret_cast<Smem<DA> *>(smem_raw);
+  pdl_wait();  // nothing is read before the previous kernel on the stream is done
+  pdl_allow_next();
   const int splits = p.Dc / DCT;
   const int unit = blockIdx.x / splits, dc0 = DCT * (blockIdx.x - unit * splits);
   Unit w;
@@ -369,12 +375,10 @@ static cudaError_t launch_scan_t(const Scan &p, int units, cudaStream_t stream) 
   cudaError_t e;
   if (p.out) {
     if ((e = set_smem_once(scan_kernel<T, TO, DA, true>, bytes, f1)) != cudaSuccess) return e;
-    scan_kernel<T, TO, DA, true><<<grid, 256, bytes, stream>>>(p);
-  } else {
-    if ((e = set_smem_once(scan_kernel<T, T, DA, false>, bytes, f0)) != cudaSuccess) return e;
-    scan_kernel<T, T, DA, false><<<grid, 256, bytes, stream>>>(p);
+    return launch_pdl(scan_kernel<T, TO, DA, true>, dim3(grid), dim3(256), bytes, stream, p);
   }
-  return cudaGetLastError();
+  if ((e = set_smem_once(scan_kernel<T, T, DA, false>, bytes, f0)) != cudaSuccess) return e;
+  return launch_pdl(scan_kernel<T, T, DA, false>, dim3(grid), dim3(256), bytes, stream, p);
 }
 
 cudaError_t launch_scan(const Scan &p, int units, int dtype, int out_dtype, cudaStream_t stream) {
@@ -392,6 +396,8 @@ cudaError_t launch_scan(const Scan &p, int units, int dtype, int out_dtype, cuda
 template <typename TO>
 __global__ void __launch_bounds__(256)
 group_sum_kernel(const float *__restrict__ part, TO *__restrict__ out, size_t quads, int D, int G) {
+  pdl_wait();  // nothing is read before the previous kernel on the stream is done
+  pdl_allow_next();
   const size_t x = (size_t)blockIdx.x * 256 + threadIdx.x;
   if (x >= quads) return;
   const size_t row = x / (D / 4), d = 4 * (x - row * (D / 4));
@@ -477,16 +483,15 @@ static cudaError_t run_scan(const Scan &p, bool tc, int units, int dtype, int ou
 static cudaError_t run_plan(Scan &p, Prefix &x, const Layout &l, unsigned char *ws, cudaStream_t stream) {
   int32_t *first_seg = reinterpret_cast<int32_t *>(ws + l.first_seg);
   int4 *units = reinterpret_cast<int4 *>(ws + l.units);
-  plan_segments_kernel<<<1, 1024, 0, stream>>>(p.cu, p.N, p.T, l.L, (int)l.max_seg, first_seg, units, p.status);
   p.units = units;
   x.first_seg = first_seg;
-  return cudaGetLastError();
+  return launch_pdl(plan_segments_kernel, dim3(1), dim3(1024), 0, stream, p.cu, p.N, p.T, l.L, (int)l.max_seg,
+                    first_seg, units, p.status);
 }
 
 static cudaError_t run_prefix(const Prefix &p, cudaStream_t stream) {
   const unsigned grid = (unsigned)p.N * (unsigned)p.Hv * (unsigned)((p.Da / 32) * (p.Dc / 32));
-  prefix_kernel<<<grid, 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(prefix_kernel, dim3(grid), dim3(256), 0, stream, p);
 }
 
 }  // namespace lin
@@ -552,11 +557,12 @@ cudaError_t launch_linear_backward(const void *q, const void *k, const void *v, 
     if (r != cudaSuccess || !grouped) return r;
     const size_t quads = (size_t)T * Hqk * Dk / 4;
     const unsigned blocks = (unsigned)((quads + 255) / 256);
+    const float *from = part;
     if (dtype == GDN_DTYPE_BF16)
-      group_sum_kernel<<<blocks, 256, 0, stream>>>(part, static_cast<__nv_bfloat16 *>(out), quads, Dk, Hv / Hqk);
-    else
-      group_sum_kernel<<<blocks, 256, 0, stream>>>(part, static_cast<float *>(out), quads, Dk, Hv / Hqk);
-    return cudaGetLastError();
+      return launch_pdl(group_sum_kernel<__nv_bfloat16>, dim3(blocks), dim3(256), 0, stream, from,
+                        static_cast<__nv_bfloat16 *>(out), quads, Dk, Hv / Hqk);
+    return launch_pdl(group_sum_kernel<float>, dim3(blocks), dim3(256), 0, stream, from, static_cast<float *>(out),
+                      quads, Dk, Hv / Hqk);
   };
 
   Scan p = base;  // S, for dq

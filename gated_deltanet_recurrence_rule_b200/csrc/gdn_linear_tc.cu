@@ -209,7 +209,7 @@ constexpr uint32_t STAGE = 3 * TILE;
 constexpr uint32_t OFF_X = 2 * STAGE;
 constexpr uint32_t OFF_W = OFF_X + TILE;
 constexpr uint32_t OFF_BAR = OFF_W + ((sizeof(Weights) + 15) / 16) * 16;
-constexpr uint32_t OFF_CTL = OFF_BAR + 240;  // TMEM base, control words
+constexpr uint32_t OFF_CTL = OFF_BAR + 256;  // TMEM base, control words
 constexpr uint32_t OFF_UNIT = OFF_CTL + 32;  // the unit, for the end of the X warps
 constexpr uint32_t SMEM_OUT = OFF_UNIT + 32;
 static_assert(SMEM_OUT <= 232448, "shared memory of a CTA");
@@ -221,8 +221,8 @@ constexpr uint32_t R_P = 0, T_PB = 0, R_O = 128, T_VH = 256, T_VM = 320, R_DX = 
 __host__ __device__ constexpr uint32_t pcol(int kk) { return 64 * (kk >> 2) + 8 * (kk & 3); }  // of T_PB
 
 enum { B_FULL = 0, B_EMPTY = 2, B_P = 4, B_PB = 6, B_V = 7, B_VFREE = 9, B_DX = 11, B_DXFREE = 12, B_OI = 13,
-       B_OA = 14, B_OFREE = 15, B_X = 16, B_FIX = 17, B_DRAIN = 18, B_EMPTYA = 19, B_OUT = 21, B_OUTFREE = 22, B_X0 = 23, B_VL = 25, B_VUSED = 27, NBAR = 29 };
-static_assert(NBAR * 8 <= 240, "barrier area");
+       B_OA = 14, B_OFREE = 15, B_X = 16, B_FIX = 17, B_DRAIN = 18, B_EMPTYA = 19, B_OUT = 21, B_X0 = 23, B_VL = 25, B_VUSED = 27, B_DXO = 29, NBAR = 31 };
+static_assert(NBAR * 8 <= 256, "barrier area");
 
 // One CTA per (segment, head).  Only X <- lam^len X + dX is carried from chunk to
 // chunk; dX, P and the rest of a chunk do not wait for the one before, except for the
@@ -233,7 +233,7 @@ static_assert(NBAR * 8 <= 240, "barrier area");
 //                wanted, writes it into a half's buffer when the first two have been used
 //   warps 16-23  P to its causal bf16 form
 //   warps 24-31  scale A X^T in place (the product with P then adds to it), and put the
-//                outputs where the chunk's A tile was
+//                outputs where the chunk's A tile was (fp32: A and B tiles)
 //   warp 2 stores them from there by TMA (a direct store of 32 rows by a warp is 32
 //   scattered pieces, about 85 cycles of the load-store unit); warp 1 issues P, A X^T
 //   and the product with P; warp 3 issues dX.
@@ -248,6 +248,8 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     prefetch_tensormap(&tm_c);
     prefetch_tensormap(&tm_o);
   }
+  pdl_wait();  // nothing is read before the previous kernel on the stream is done
+  pdl_allow_next();
   Unit u;
   if (!get_unit(p, blockIdx.x, u)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -266,8 +268,9 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
       // one arrival per warp of the group that signals; a stage is freed by both issuers
       const bool eight = i == B_DXFREE || i == B_OFREE || i == B_X || i == B_OUT || i == B_X0 || i == B_X0 + 1;
       const bool four = i == B_V || i == B_V + 1 || i == B_VL || i == B_VL + 1 || i == B_FIX;
-      const bool two = i == B_EMPTY || i == B_EMPTY + 1 || i == B_DRAIN;
-      mbar_init(bar(i), i == B_PB ? 16 : eight ? 8 : four ? 4 : two ? 2 : 1);
+      const int empty = sizeof(TO) == 4 ? 3 : 2;  // fp32: its B tile's place is stored from, too
+      mbar_init(bar(i), i == B_PB ? 16 : eight ? 8 : four ? 4 : i == B_EMPTY || i == B_EMPTY + 1 ? empty :
+                        i == B_DRAIN ? 2 : 1);
     }
     ctl[CTL_ABORT] = 0;
     ctl[CTL_LIMIT] = 4000000;  // until warp 2 has read the header
@@ -402,6 +405,7 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
           mma_commit(bar((j + 2 < parts ? B_VUSED : B_VFREE) + hf));  // used by two terms; by all
           if (j == parts - 1) {
             mma_commit(bar(B_DX));
+            mma_commit(bar(B_DXO + s));
             mma_commit(bar(B_EMPTY + s));
           }
         }
@@ -419,27 +423,24 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     // ------------------------------------------------------------ stores
     if (lane == 0) ctl[CTL_LIMIT] = wait_limit(p.status);
     __syncwarp();
-    constexpr int BOXES = sizeof(TO) / 2;  // of 128 bytes a row, for 64 columns
+    constexpr int BOXES = 4 * (int)sizeof(TO);  // of 32 rows by 128 bytes
     for (int ci = 0; ci < nch; ++ci) {
       const int c = chunk_of(ci), s = ci & 1;
       const int len = c == nch - 1 ? tail : CH;
+      if (!warp_wait(B_OUT, ci & 1)) break;
+      if (lane == 0) {
 #pragma unroll 1
-      for (int j = 0; j < BOXES; ++j) {
-        if (!warp_wait(B_OUT, (BOXES * ci + j) & 1)) break;
-        if (lane == 0) {
-          // boxes of 32 rows that end inside the sequence
-#pragma unroll 1
-          for (int i = 0; i < 8; ++i) {
-            const int hf = i >> 2, r = 32 * (i & 3);
-            if (r + 32 <= len && 64 * hf < p.Dc)
-              tma_store_3d(&tm_o, sb + s * STAGE + hf * 16384 + r * 128, 64 * hf + j * 32, u.h, u.t0 + c * CH + r);
-          }
-          bulk_commit_group();
-          bulk_wait_read_all();
-          mbar_arrive(bar(j + 1 < BOXES ? B_OUTFREE : B_EMPTYA + s));
+        for (int i = 0; i < BOXES; ++i) {
+          const int hf = (i >> 2) & 1, r = 32 * (i & 3), col = 64 * hf + 32 * (i >> 3);
+          if (r + 32 <= len && 64 * hf < p.Dc)  // boxes that end inside the sequence
+            tma_store_3d(&tm_o, sb + s * STAGE + (i >> 2) * 16384 + r * 128, col, u.h, u.t0 + c * CH + r);
         }
-        __syncwarp();
+        bulk_commit_group();
+        bulk_wait_read_all();
+        mbar_arrive(bar(B_EMPTYA + s));
+        if (sizeof(TO) == 4) mbar_arrive(bar(B_EMPTY + s));
       }
+      __syncwarp();
     }
     if (lane == 0) bulk_wait_all();
   } else if (warp >= 4 && warp < 8) {
@@ -637,7 +638,6 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
     const int hf = (warp - 24) >> 2;                // half of the columns of O
     const int lq = warp & 3, row = 32 * lq + lane;  // TMEM lane: token
     const uint32_t tl = tmem + ((uint32_t)(32 * lq) << 16) + R_O + 64 * hf;
-    constexpr int COLS = 128 / sizeof(TO);          // columns of a 128-byte row of a store
     for (int ci = 0; ci < nch; ++ci) {
       const int c = chunk_of(ci), s = ci & 1;
       const uint32_t ph = ci & 1;
@@ -658,44 +658,41 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
       tc_fence_before();
       arrive(B_PB);
       if (!warp_wait(B_OA, ph)) break;
-      // rows of this warp: a 4096-byte box of 32 rows at its place in the A tile
+      if (sizeof(TO) == 4 && !warp_wait(B_DXO + s, (ci >> 1) & 1)) break;  // dX has used the B tile
+      // rows of this warp: boxes of 32 rows by 128 bytes, 32 (fp32) or 64 columns, at their
+      // places in the tiles
       unsigned char *box = smem + s * STAGE + hf * 16384 + lq * 4096;
       const bool whole = 32 * lq + 32 <= len;
-      bool ok = true;
-#pragma unroll 1
-      for (int j = 0; j < 64; j += COLS) {
-        // (fp32: the second 32 columns take the place of the first once those are stored)
-        if (j > 0 && !(ok = warp_wait(B_OUTFREE, ph))) break;
 #pragma unroll
-        for (int i = 0; i < COLS; i += 32) {
-          float v[32];
-          tmem_ld32(tl + j + i, v);
-          tmem_wait_ld();
-          if (j + i == 32) {
-            tc_fence_before();
-            arrive(B_OFREE);
-          }
-          constexpr int W = 32 * sizeof(TO) / 4;  // words
-          uint32_t w[W];
-#pragma unroll
-          for (int k = 0; k < W; ++k)
-            w[k] = sizeof(TO) == 2 ? pack_bf16x2(v[(2 * k) % 32], v[(2 * k + 1) % 32]) : __float_as_uint(v[k]);
-          if (whole) {
-#pragma unroll
-            for (int k = 0; k < W; k += 4)
-              *reinterpret_cast<uint4 *>(box + sw128_off(lane, i * (int)sizeof(TO) / 16 + k / 4)) =
-                  make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
-          } else if (row < len && 64 * hf < p.Dc) {  // the rows after belong to the next sequence
-            TO *o = static_cast<TO *>(p.out) + ((size_t)(u.t0 + c * CH + row) * p.Hv + u.h) * p.Dc + 64 * hf + j + i;
-#pragma unroll
-            for (int k = 0; k < W; k += 4)
-              *reinterpret_cast<uint4 *>(o + k * 4 / (int)sizeof(TO)) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
-          }
+      for (int j = 0; j < 64; j += 32) {
+        float v[32];
+        tmem_ld32(tl + j, v);
+        tmem_wait_ld();
+        if (j == 32) {
+          tc_fence_before();
+          arrive(B_OFREE);
         }
-        fence_proxy_async_smem();
-        arrive(B_OUT);
+        constexpr int W = 32 * sizeof(TO) / 4;  // words
+        uint32_t w[W];
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+          w[k] = sizeof(TO) == 2 ? pack_bf16x2(v[(2 * k) % 32], v[(2 * k + 1) % 32]) : __float_as_uint(v[k]);
+        unsigned char *at = sizeof(TO) == 4 ? box + (j / 32) * TILE : box;
+        const int ch0 = sizeof(TO) == 4 ? 0 : j / 8;
+        if (whole) {
+#pragma unroll
+          for (int k = 0; k < W; k += 4)
+            *reinterpret_cast<uint4 *>(at + sw128_off(lane, ch0 + k / 4)) =
+                make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+        } else if (row < len && 64 * hf < p.Dc) {  // the rows after belong to the next sequence
+          TO *o = static_cast<TO *>(p.out) + ((size_t)(u.t0 + c * CH + row) * p.Hv + u.h) * p.Dc + 64 * hf + j;
+#pragma unroll
+          for (int k = 0; k < W; k += 4)
+            *reinterpret_cast<uint4 *>(o + k * 4 / (int)sizeof(TO)) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+        }
       }
-      if (!ok) break;
+      fence_proxy_async_smem();
+      arrive(B_OUT);
     }
   }
   tc_fence_before();
@@ -727,6 +724,8 @@ scan_state_tc_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_cons
     prefetch_tensormap(&tm_b);
     prefetch_tensormap(&tm_c);
   }
+  pdl_wait();  // nothing is read before the previous kernel on the stream is done
+  pdl_allow_next();
   Unit u;
   if (!get_unit(p, blockIdx.x, u)) return;
   if (u.last && (u.first || !p.xf)) return;  // nothing starts from its end
@@ -909,16 +908,14 @@ cudaError_t launch_scan_tc(const Scan &p, int units, int out_dtype, cudaStream_t
   cudaError_t e;
   if (!p.out) {
     if ((e = set_smem_once(scan_state_tc_kernel, SMEM_STATE, f0)) != cudaSuccess) return e;
-    scan_state_tc_kernel<<<(unsigned)units, NTHREADS, SMEM_STATE, stream>>>(mb, mc, p);
-    return cudaGetLastError();
+    return launch_pdl(scan_state_tc_kernel, dim3((unsigned)units), dim3(NTHREADS), SMEM_STATE, stream, mb, mc, p);
   }
   if (!make_map(&ma, p.a, p.Ha, p.T, p.Da) || !make_map(&mo, p.out, p.Hv, p.T, p.Dc, out_dtype == GDN_DTYPE_FP32, 32))
     return cudaErrorInvalidValue;
   auto go = [&](auto kern, std::atomic<bool>(&flags)[64]) {
     const cudaError_t r = set_smem_once(kern, SMEM_OUT, flags);
     if (r != cudaSuccess) return r;
-    kern<<<(unsigned)units, NTHREADS_O, SMEM_OUT, stream>>>(ma, mb, mc, mo, p);
-    return cudaGetLastError();
+    return launch_pdl(kern, dim3((unsigned)units), dim3(NTHREADS_O), SMEM_OUT, stream, ma, mb, mc, mo, p);
   };
   if (out_dtype == GDN_DTYPE_BF16)
     return p.back ? go(scan_out_tc_kernel<__nv_bfloat16, true>, f1) : go(scan_out_tc_kernel<__nv_bfloat16, false>, f2);
