@@ -15,6 +15,7 @@
 // state S0, which is read once and left as it is.
 #include "gdn_common.cuh"
 #include "gdn_rows.cuh"
+#include "gdn_sm100.cuh"
 
 namespace gdn {
 namespace tree {
@@ -76,8 +77,7 @@ struct Layout {
   static constexpr int O = MP * LDU * 4;                       // [MP][LDU]
   static constexpr int V = XB > 2 * O ? XB : 2 * O;            // [MP][DV] T
   // by node i and place s along its path (0: the parent), j the ancestor there
-  static constexpr int E = V + MP * DV * (int)sizeof(T);       // [MP][MP] fp32 E_ij
-  static constexpr int AC = E + MP * MP * 4;                   // [MP][MP] {E_ij (k_j . k_i), E_ij (k_j . q_i)}
+  static constexpr int AC = V + MP * DV * (int)sizeof(T);      // [MP][MP] {E_ij (k_j . k_i), E_ij (k_j . q_i)}
   static constexpr int IDX = AC + MP * MP * 8;                 // [MP][MP] bytes: j
   static constexpr int S = IDX + MP * MP;                      // per-node scalars
   static constexpr int BYTES = S + MP * 4 * 11 + 16;
@@ -100,7 +100,7 @@ __device__ __forceinline__ void cp_async_16(void *dst, const void *src) {
 // lie in its order, four to a load.  Every global load of the CTA is issued before the first is waited for.
 // Bound: HBM, one read of each state; the products are 4 M flops an element.
 template <typename T, typename ST, int SP, int XP, int DK, int DV, int MP>
-__global__ void __launch_bounds__(DV == 128 && MP == 64 ? 256 : 128, MP <= 32 ? 3 : 2)
+__global__ void __launch_bounds__(DV == 128 && MP == 64 ? 256 : 128, MP <= 32 ? 4 : 2)
 decode_tree_kernel(const Params p) {
   pdl_wait();  // nothing is read before the previous kernel on the stream is done
   pdl_allow_next();
@@ -108,14 +108,13 @@ decode_tree_kernel(const Params p) {
   constexpr int MT = DV / (16 * NW);   // 16-row tiles of S0 per warp
   constexpr int NX = 2 * MP / 8;       // 8-node column tiles of [k; q]^T
   constexpr int KS = DK / 16;
-  constexpr int PF = KS < 4 ? KS : 4;  // k steps of S0 in flight
+  constexpr int PF = MP <= 32 ? 2 : 4; // k steps of S0 in flight (all of it is on its way to L2)
   constexpr int MAXP = SP > XP ? SP : XP;
   using L = Layout<T, XP, DK, DV, MP>;
   extern __shared__ __align__(16) unsigned char smem[];
   __nv_bfloat16 *X = reinterpret_cast<__nv_bfloat16 *>(smem + L::X);
   float *U = reinterpret_cast<float *>(smem + L::U), *O = reinterpret_cast<float *>(smem + L::O);
   T *V = reinterpret_cast<T *>(smem + L::V);
-  float *E = reinterpret_cast<float *>(smem + L::E);
   float2 *AC = reinterpret_cast<float2 *>(smem + L::AC);
   unsigned char *idx = smem + L::IDX;
   unsigned long long *anc = reinterpret_cast<unsigned long long *>(smem + L::S);  // strict ancestors
@@ -140,6 +139,7 @@ decode_tree_kernel(const Params p) {
   }
   const ST *S = static_cast<const ST *>(p.state) + ((size_t)src * p.Hv + h) * DV * DK;
 
+  if (tid == 0) sm100::bulk_prefetch_l2(S, DV * DK * (int)sizeof(ST));
   // S0 fragments: rows 16 (warp MT + mt) + gid, + 8; columns 16 ks + 4 tig .. + 3
   float sf[PF][MT][2][4];
   auto load_ks = [&](int slot, int ks) {
@@ -218,7 +218,7 @@ decode_tree_kernel(const Params p) {
     int s = 0, a = par[i];
     for (; a >= 0; a = par[a], ++s) {
       m |= 1ull << a;
-      E[i * MP + s] = e;
+      AC[i * MP + s] = make_float2(e, e);  // E_ij, times the products below
       idx[i * MP + s] = (unsigned char)a;
       e *= alpha[a];
     }
@@ -278,7 +278,7 @@ decode_tree_kernel(const Params p) {
   // [k; q] k^T -> AC (ancestors only)
   for (int mt = warp; mt < 2 * MP / 16; mt += NW) {
     float acc[MP / 8][4] = {};
-#pragma unroll 2
+#pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       uint32_t a[XP][4];
 #pragma unroll
@@ -305,7 +305,7 @@ decode_tree_kernel(const Params p) {
         const float y = acc[n][e] * (rn[r] * rn[c]);
         if (anc[i] >> c & 1) {
           const int s = i * MP + __popcll(anc[i] >> c) - 1;  // its place on the path
-          (r < MP ? AC[s].x : AC[s].y) = E[s] * y;
+          (r < MP ? AC[s].x : AC[s].y) *= y;
         } else if (i == c && r >= MP) {
           cself[i] = y;
         }
