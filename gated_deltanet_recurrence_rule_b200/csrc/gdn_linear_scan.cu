@@ -12,7 +12,6 @@ namespace gdn {
 namespace lin {
 
 using chunk::mma_tf32_16x8x8;
-using chunk::to_tf32;
 
 // ---------------------------------------------------------------- plan
 // The segments of the packed sequences (an empty one has one, of no tokens), by one
@@ -168,21 +167,28 @@ __global__ void __launch_bounds__(256) prefix_kernel(const Prefix p) {
 
 // ---------------------------------------------------------------- the scan
 // d += A (16 x 8) B (8 x 8) in tf32 with the operands split in two terms (three
-// products, about fp32) where they are not exact in tf32 (EXA, EXB: bf16 inputs).
+// products, about fp32) where they are not exact in tf32 (EXA, EXB: bf16 inputs).  The
+// first term is the value rounded to 11 bits, by integers (cvt.rna.tf32 was what bound
+// the kernel: fp32 prefill of 8192 tokens 2.35 ms against 1.3); the second what that
+// leaves, of which the tensor core takes 11 of 12 bits.  A NaN stays in the second.
+template <bool EX>
+__device__ __forceinline__ uint32_t first_term(float x) {
+  return EX ? __float_as_uint(x) : (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+}
 template <bool EXA, bool EXB>
 __device__ __forceinline__ void mma_split(float *d, const float *a, const float *b) {
   uint32_t ah[4], bh[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) ah[i] = to_tf32(a[i]);
+  for (int i = 0; i < 4; ++i) ah[i] = first_term<EXA>(a[i]);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) bh[i] = to_tf32(b[i]);
+  for (int i = 0; i < 2; ++i) bh[i] = first_term<EXB>(b[i]);
   if (!EXB) {
-    const uint32_t bl[2] = {to_tf32(b[0] - __uint_as_float(bh[0])), to_tf32(b[1] - __uint_as_float(bh[1]))};
+    const uint32_t bl[2] = {__float_as_uint(b[0] - __uint_as_float(bh[0])), __float_as_uint(b[1] - __uint_as_float(bh[1]))};
     mma_tf32_16x8x8(d, ah, bl);
   }
   if (!EXA) {
-    const uint32_t al[4] = {to_tf32(a[0] - __uint_as_float(ah[0])), to_tf32(a[1] - __uint_as_float(ah[1])),
-                            to_tf32(a[2] - __uint_as_float(ah[2])), to_tf32(a[3] - __uint_as_float(ah[3]))};
+    const uint32_t al[4] = {__float_as_uint(a[0] - __uint_as_float(ah[0])), __float_as_uint(a[1] - __uint_as_float(ah[1])),
+                            __float_as_uint(a[2] - __uint_as_float(ah[2])), __float_as_uint(a[3] - __uint_as_float(ah[3]))};
     mma_tf32_16x8x8(d, al, bh);
   }
   mma_tf32_16x8x8(d, ah, bh);
@@ -196,13 +202,55 @@ struct Smem {
   float a[C][DA + 4], b[C][DA + 4], c[C][DCT + 8], P[C][C + 4], X[DCT][DA + 4], pw[C + 1];
 };
 
-// One CTA per (segment, head, 64 columns of out), 8 warps.  Per chunk of 64
+// 4 elements on their way from global memory.
+template <typename T> struct Quad;
+template <> struct Quad<float> {
+  float4 x;
+  __device__ __forceinline__ void load(const float *p) { x = *reinterpret_cast<const float4 *>(p); }
+  __device__ __forceinline__ void zero() { x = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ float4 get() const { return x; }
+};
+template <> struct Quad<__nv_bfloat16> {
+  uint2 x;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { x = *reinterpret_cast<const uint2 *>(p); }
+  __device__ __forceinline__ void zero() { x = make_uint2(0u, 0u); }
+  __device__ __forceinline__ float4 get() const {
+    return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
+                       __uint_as_float(x.y & 0xffff0000u));
+  }
+};
+// A thread's part of a chunk's 64 rows x W columns, from row `base` on; rows past `len`
+// read as zeros.
+template <typename T, int W, int NTH>
+struct TilePart {
+  static constexpr int N = C * W / 4 / NTH;
+  Quad<T> q[N];
+  __device__ __forceinline__ void load(const T *base, size_t step, int len, int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int x = tid + i * NTH, r = x / (W / 4), d = 4 * (x - r * (W / 4));
+      if (r < len) q[i].load(base + (size_t)r * step + d);
+      else q[i].zero();
+    }
+  }
+  __device__ __forceinline__ void store(float *dst, int ld, int tid) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int x = tid + i * NTH, r = x / (W / 4), d = 4 * (x - r * (W / 4));
+      *reinterpret_cast<float4 *>(dst + r * ld + d) = q[i].get();
+    }
+  }
+};
+
+// One CTA per (segment, head, 64 columns of out), 16 warps.  Per chunk of 64
 // tokens: P = (A B^T) . lam^{|t-s|}; out = s_intra P C + s_inter lam^{p+1} A X^T;
 // X <- lam^len X + (w C)^T B.  X stays in fp32 accumulator registers, with a copy
-// in shared memory as an operand.  Bound: the tf32 products (three for each fp32
-// one).  This form serves fp32 inputs, fp32 outputs and head dim 64.
+// in shared memory as an operand; the next chunk's tiles are on their way in registers
+// meanwhile.  Bound: the tf32 products (three for each fp32 one) and their operands'
+// shared-memory reads.  This form serves fp32 inputs and fp32 outputs.
+constexpr int NTHREADS = 512;
 template <typename T, typename TO, int DA, bool OUT>
-__global__ void __launch_bounds__(256) scan_kernel(const Scan p) {
+__global__ void __launch_bounds__(NTHREADS) scan_kernel(const Scan p) {
   constexpr bool EX = sizeof(T) == 2;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem<DA> &s = *reinterpret_cast<Smem<DA> *>(smem_raw);
@@ -214,92 +262,82 @@ __global__ void __launch_bounds__(256) scan_kernel(const Scan p) {
   if (!get_unit(p, unit, w)) return;
   if (!OUT && w.last && (w.first || !p.xf)) return;  // nothing starts from its end
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
-  const int ha = w.h / (p.Hv / p.Ha), hb = w.h / (p.Hv / p.Hb), hc = w.h / (p.Hv / p.Hc);
   const float gh = head_decay(p, w.h);
+  const int mt = warp >> 2, nq = warp & 3;  // this warp's 16 rows and quarter of the columns
+  constexpr int NX = DA / 32;               // 8-column tiles of X per warp
+  const int nch = (w.t1 - w.t0 + C - 1) / C;
+  auto chunk_of = [&](int ci) { return p.back ? nch - 1 - ci : ci; };
+
+  TilePart<T, DA, NTHREADS> ta, tb;
+  TilePart<T, DCT, NTHREADS> tc;
+  auto fetch = [&](int ci) {
+    const int t0 = w.t0 + chunk_of(ci) * C, len = min(C, w.t1 - t0);
+    auto at = [&](const void *base, int H, int D) {
+      return static_cast<const T *>(base) + ((size_t)t0 * H + w.h / (p.Hv / H)) * D;
+    };
+    if (OUT) ta.load(at(p.a, p.Ha, DA), (size_t)p.Ha * DA, len, tid);
+    tb.load(at(p.b, p.Hb, DA), (size_t)p.Hb * DA, len, tid);
+    tc.load(at(p.c, p.Hc, p.Dc) + dc0, (size_t)p.Hc * p.Dc, len, tid);
+  };
+  if (nch > 0) fetch(0);
   if (tid <= C) s.pw[tid] = expf(gh * (float)tid);
-  const int mt = warp >> 1, nh = warp & 1;  // this warp's 16 rows and half of the columns
-  constexpr int NX = DA / 16;               // 8-column tiles of X per warp
 
   float X[NX][4];
-  if (OUT) {
 #pragma unroll
-    for (int n = 0; n < NX; ++n)
+  for (int n = 0; n < NX; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        X[n][e] = start_state(p, w, dc0 + 16 * mt + gid + 8 * (e >> 1), 8 * (nh * NX + n) + 2 * tig + (e & 1));
-  } else {
-#pragma unroll
-    for (int n = 0; n < NX; ++n) X[n][0] = X[n][1] = X[n][2] = X[n][3] = 0.f;
-  }
+    for (int e = 0; e < 4; ++e)
+      X[n][e] = OUT ? start_state(p, w, dc0 + 16 * mt + gid + 8 * (e >> 1), 8 * (nq * NX + n) + 2 * tig + (e & 1)) : 0.f;
   auto put_x = [&]() {
 #pragma unroll
     for (int n = 0; n < NX; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        s.X[16 * mt + gid + 8 * (e >> 1)][8 * (nh * NX + n) + 2 * tig + (e & 1)] = X[n][e];
+        s.X[16 * mt + gid + 8 * (e >> 1)][8 * (nq * NX + n) + 2 * tig + (e & 1)] = X[n][e];
   };
   if (OUT) put_x();
 
-  const int nch = (w.t1 - w.t0 + C - 1) / C;
   for (int ci = 0; ci < nch; ++ci) {
-    const int c = p.back ? nch - 1 - ci : ci;
-    const int t0 = w.t0 + c * C, len = min(C, w.t1 - t0);
+    const int t0 = w.t0 + chunk_of(ci) * C, len = min(C, w.t1 - t0);
     const int skip = p.back && w.first && ci == 0 ? 1 : 0;
     __syncthreads();  // the last chunk's tiles have been used
-    auto load = [&](const void *base, int H, int h, int D, int d0, int width, float *dst, int ld) {
-      for (int x = tid; x < C * width / 4; x += 256) {
-        const int r = x / (width / 4), d = 4 * (x - r * (width / 4));
-        float y[4] = {0.f, 0.f, 0.f, 0.f};  // rows past the segment read as zeros
-        if (r < len) load4(static_cast<const T *>(base) + ((size_t)(t0 + r) * H + h) * D + d0 + d, y);
-        *reinterpret_cast<float4 *>(dst + r * ld + d) = make_float4(y[0], y[1], y[2], y[3]);
-      }
-    };
-    if (OUT) load(p.a, p.Ha, ha, DA, 0, DA, &s.a[0][0], DA + 4);
-    load(p.b, p.Hb, hb, DA, 0, DA, &s.b[0][0], DA + 4);
-    load(p.c, p.Hc, hc, p.Dc, dc0, DCT, &s.c[0][0], DCT + 8);
+    if (OUT) ta.store(&s.a[0][0], DA + 4, tid);
+    tb.store(&s.b[0][0], DA + 4, tid);
+    tc.store(&s.c[0][0], DCT + 8, tid);
     __syncthreads();
+    if (ci + 1 < nch) fetch(ci + 1);
     if (OUT) {
-      // P, rows t of tile mt, columns s of half nh
-      float acc[4][4] = {};
-#pragma unroll 2
+      // P, rows t of tile mt, columns s of quarter nq; A X^T beside it
+      float acc[2][4] = {}, oi[2][4] = {}, oa[2][4] = {};
+#pragma unroll 4
       for (int k = 0; k < DA; k += 8) {
         const float af[4] = {s.a[16 * mt + gid][k + tig], s.a[16 * mt + gid + 8][k + tig],
                              s.a[16 * mt + gid][k + tig + 4], s.a[16 * mt + gid + 8][k + tig + 4]};
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int sc = 8 * (4 * nh + n) + gid;
-          const float bf[2] = {s.b[sc][k + tig], s.b[sc][k + tig + 4]};
+        for (int n = 0; n < 2; ++n) {
+          const int col = 8 * (2 * nq + n) + gid;
+          const float bf[2] = {s.b[col][k + tig], s.b[col][k + tig + 4]};
           mma_split<EX, EX>(acc[n], af, bf);
+          const float xf[2] = {s.X[col][k + tig], s.X[col][k + tig + 4]};
+          mma_split<EX, false>(oi[n], af, xf);
         }
       }
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int t = 16 * mt + gid + 8 * (e >> 1), sc = 8 * (4 * nh + n) + 2 * tig + (e & 1);
+          const int t = 16 * mt + gid + 8 * (e >> 1), sc = 8 * (2 * nq + n) + 2 * tig + (e & 1);
           const int d = p.back ? sc - t : t - sc;
           s.P[t][sc] = d >= 0 ? acc[n][e] * s.pw[d] : 0.f;
         }
       __syncthreads();
-      float oi[4][4] = {}, oa[4][4] = {};
-#pragma unroll 2
-      for (int k = 0; k < DA; k += 8) {
-        const float af[4] = {s.a[16 * mt + gid][k + tig], s.a[16 * mt + gid + 8][k + tig],
-                             s.a[16 * mt + gid][k + tig + 4], s.a[16 * mt + gid + 8][k + tig + 4]};
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int dc = 8 * (4 * nh + n) + gid;
-          const float bf[2] = {s.X[dc][k + tig], s.X[dc][k + tig + 4]};
-          mma_split<EX, false>(oi[n], af, bf);
-        }
-      }
-#pragma unroll 2
+#pragma unroll 4
       for (int k = 0; k < C; k += 8) {
         const float af[4] = {s.P[16 * mt + gid][k + tig], s.P[16 * mt + gid + 8][k + tig],
                              s.P[16 * mt + gid][k + tig + 4], s.P[16 * mt + gid + 8][k + tig + 4]};
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int dc = 8 * (4 * nh + n) + gid;
+        for (int n = 0; n < 2; ++n) {
+          const int dc = 8 * (2 * nq + n) + gid;
           const float bf[2] = {s.c[k + tig][dc], s.c[k + tig + 4][dc]};
           mma_split<false, EX>(oa[n], af, bf);
         }
@@ -311,8 +349,8 @@ __global__ void __launch_bounds__(256) scan_kernel(const Scan p) {
         if (t >= len) continue;
         const float wi = p.s_inter * s.pw[(p.back ? len - 1 - t : t) + 1 - skip];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          TO *o = out + ((size_t)(t0 + t) * p.Hv + w.h) * p.Dc + dc0 + 8 * (4 * nh + n) + 2 * tig;
+        for (int n = 0; n < 2; ++n) {
+          TO *o = out + ((size_t)(t0 + t) * p.Hv + w.h) * p.Dc + dc0 + 8 * (2 * nq + n) + 2 * tig;
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             o[e] = from_f32<TO>(fmaf(wi, oi[n][2 * r + e], p.s_intra * oa[n][2 * r + e]));
@@ -323,7 +361,7 @@ __global__ void __launch_bounds__(256) scan_kernel(const Scan p) {
     // (the chunk's sum on its own: tensor cores cut what an addition shifts out, which
     // over many additions to a large X would be a drift)
     float dx[NX][4] = {};
-#pragma unroll 2
+#pragma unroll 4
     for (int k = 0; k < C; k += 8) {
       float wt[2];
 #pragma unroll
@@ -335,7 +373,7 @@ __global__ void __launch_bounds__(256) scan_kernel(const Scan p) {
                            wt[1] * s.c[k + tig + 4][16 * mt + gid], wt[1] * s.c[k + tig + 4][16 * mt + gid + 8]};
 #pragma unroll
       for (int n = 0; n < NX; ++n) {
-        const int da = 8 * (nh * NX + n) + gid;
+        const int da = 8 * (nq * NX + n) + gid;
         const float bf[2] = {s.b[k + tig][da], s.b[k + tig + 4][da]};
         mma_split<false, EX>(dx[n], af, bf);
       }
@@ -345,10 +383,7 @@ __global__ void __launch_bounds__(256) scan_kernel(const Scan p) {
     for (int n = 0; n < NX; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) X[n][e] = fmaf(lx, X[n][e], dx[n][e]);
-    if (OUT) {
-      __syncthreads();  // X has been used
-      put_x();
-    }
+    if (OUT) put_x();  // (its readers have passed the barrier after P)
   }
   const bool fin = OUT && w.first && w.last && p.xf;
   if (OUT && !fin) return;
@@ -360,7 +395,7 @@ __global__ void __launch_bounds__(256) scan_kernel(const Scan p) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const size_t at = base + (size_t)(dc0 + 16 * mt + gid + 8 * (e >> 1)) * p.Da +
-                        8 * (nh * NX + n) + 2 * tig + (e & 1);
+                        8 * (nq * NX + n) + 2 * tig + (e & 1);
       if (fin && p.x_bf16) static_cast<__nv_bfloat16 *>(p.xf)[at] = __float2bfloat16_rn(f * X[n][e]);
       else (fin ? static_cast<float *>(p.xf) : p.seg_state)[at] = f * X[n][e];
     }
@@ -375,10 +410,10 @@ static cudaError_t launch_scan_t(const Scan &p, int units, cudaStream_t stream) 
   cudaError_t e;
   if (p.out) {
     if ((e = set_smem_once(scan_kernel<T, TO, DA, true>, bytes, f1)) != cudaSuccess) return e;
-    return launch_pdl(scan_kernel<T, TO, DA, true>, dim3(grid), dim3(256), bytes, stream, p);
+    return launch_pdl(scan_kernel<T, TO, DA, true>, dim3(grid), dim3(NTHREADS), bytes, stream, p);
   }
   if ((e = set_smem_once(scan_kernel<T, T, DA, false>, bytes, f0)) != cudaSuccess) return e;
-  return launch_pdl(scan_kernel<T, T, DA, false>, dim3(grid), dim3(256), bytes, stream, p);
+  return launch_pdl(scan_kernel<T, T, DA, false>, dim3(grid), dim3(NTHREADS), bytes, stream, p);
 }
 
 cudaError_t launch_scan(const Scan &p, int units, int dtype, int out_dtype, cudaStream_t stream) {
