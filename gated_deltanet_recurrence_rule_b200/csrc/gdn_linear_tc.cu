@@ -502,6 +502,7 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
       arrive(B_X0);
     }
     bool ok = warp_wait(B_X0, 0);
+    if (!ok) mbar_wait_landed(bar(B_X0), 0, 50000000ull);  // the copies land before the CTA can exit
     if (ok && some) {
       const unsigned char *at = smem + STAGE + slot;
       if (bf) {

@@ -47,6 +47,59 @@ def commit(lib, **kw):
                                a["sdt"], a["form"], a["status"], None)
 
 
+def prefill(lib, **kw):
+    a = dict(q=P, k=P, v=P, g=P, cu=P, N=1, T=16, dt=0, odt=1, sdt=1, scale=1.0, s0=None, sf=None, o=P, ws=P,
+             wsb=1 << 20, **DIMS)
+    a.update(kw)
+    return lib.gdn_linear_prefill(a["q"], a["k"], a["v"], a["g"], a["cu"], a["N"], a["T"], a["Hqk"], a["Hv"], a["Dk"],
+                                  a["Dv"], a["dt"], a["odt"], a["sdt"], a["scale"], a["s0"], a["sf"], a["o"], a["ws"],
+                                  a["wsb"], None)
+
+
+def backward(lib, **kw):
+    a = dict(q=P, k=P, v=P, g=P, cu=P, N=1, T=16, dt=0, scale=1.0, s0=None, do=P, dsf=None, dq=P, dk=P, dv=P, ds0=None,
+             ws=P, wsb=1 << 20, **DIMS)
+    a.update(kw)
+    return lib.gdn_linear_prefill_backward(a["q"], a["k"], a["v"], a["g"], a["cu"], a["N"], a["T"], a["Hqk"], a["Hv"],
+                                           a["Dk"], a["Dv"], a["dt"], a["scale"], a["s0"], a["do"], a["dsf"], a["dq"],
+                                           a["dk"], a["dv"], a["ds0"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("call", [prefill, backward])
+def test_packed_refusals(lib, call):
+    assert call(lib, Hv=5) == BAD and call(lib, Hqk=0) == BAD and call(lib, dt=2) == BAD
+    assert call(lib, Dk=96) == UNSUP and call(lib, Dv=256) == UNSUP and call(lib, Dv=0) == BAD
+    assert call(lib, N=-1) == BAD and call(lib, T=-1) == BAD and call(lib, T=2 ** 31) == BAD
+    assert call(lib, N=0, T=0) == OK and call(lib, N=0, T=5) == BAD
+    assert call(lib, N=2 ** 30, T=16) == UNSUP         # more CTAs than a grid takes
+    for name in ("q", "k", "v", "g", "cu"):
+        assert call(lib, **{name: None}) == BAD
+    for name in ("q", "k", "v"):
+        assert call(lib, **{name: P + 8}) == BAD       # bases are 16-byte aligned
+    assert call(lib, g=P + 2) == BAD and call(lib, cu=P + 2) == BAD and call(lib, s0=P + 8) == BAD
+    assert call(lib, ws=None) == api.GDN_ERR_WORKSPACE and call(lib, ws=P + 16) == api.GDN_ERR_WORKSPACE
+    assert call(lib, wsb=255) == api.GDN_ERR_WORKSPACE
+    need = lib.gdn_linear_prefill_workspace_size(3, 9000, 2, 6, 64, 64, 0, int(call is backward))
+    assert need > 256
+    assert call(lib, N=3, T=9000, wsb=need - 1) == api.GDN_ERR_WORKSPACE
+
+
+def test_prefill_and_backward_outputs_are_checked(lib):
+    assert prefill(lib, o=None) == BAD and prefill(lib, o=P + 8) == BAD and prefill(lib, sf=P + 8) == BAD
+    assert prefill(lib, odt=2) == BAD and prefill(lib, sdt=2) == BAD
+    for name in ("do", "dq", "dk", "dv"):
+        assert backward(lib, **{name: None}) == BAD and backward(lib, **{name: P + 8}) == BAD
+    assert backward(lib, dsf=P + 8) == BAD and backward(lib, ds0=P + 8) == BAD
+
+
+def test_workspace_sizes(lib):
+    size = lib.gdn_linear_prefill_workspace_size
+    assert size(1, 16, 2, 6, 64, 64, 0, 0) >= 256
+    assert size(1, 8192, 16, 48, 128, 128, 0, 1) > size(1, 8192, 16, 48, 128, 128, 0, 0) > 256
+    assert size(1, 8192, 16, 48, 96, 128, 0, 0) == 0 and size(-1, 8, 2, 6, 64, 64, 0, 0) == 0
+    assert size(1, 8, 2, 5, 64, 64, 0, 0) == 0 and size(1, 8, 2, 6, 64, 64, 7, 0) == 0
+
+
 @pytest.mark.parametrize("call", [decode, tree, commit])
 def test_common_refusals(lib, call):
     assert call(lib, Hv=5) == BAD and call(lib, Hqk=0) == BAD and call(lib, Hv=-6) == BAD
@@ -100,3 +153,7 @@ def test_python_refuses_cpu_tensors(lib):
         api.decode_tree(x, x, v, g, None, p, s)
     with pytest.raises(ValueError, match="CUDA"):
         api.tree_commit(x, v, g, None, p, p[:, 0], s)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.linear_prefill(x[0], x[0], v[0], g)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.linear_prefill_backward(x[0], x[0], v[0], g, v[0])
