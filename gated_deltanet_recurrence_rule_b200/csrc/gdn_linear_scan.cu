@@ -168,15 +168,17 @@ __global__ void __launch_bounds__(256) prefix_kernel(const Prefix p) {
 // ---------------------------------------------------------------- the scan
 // d += A (16 x 8) B (8 x 8) in tf32 with the operands split in two terms (three
 // products, about fp32) where they are not exact in tf32 (EXA, EXB: bf16 inputs).  The
-// first term is the value rounded to 11 bits, by integers (cvt.rna.tf32 was what bound
-// the kernel: fp32 prefill of 8192 tokens 2.35 ms against 1.3); the second what that
-// leaves, of which the tensor core takes 11 of 12 bits.  A NaN stays in the second.
+// first term is the value rounded to 11 bits, by integers (with cvt.rna.tf32
+// in its place, 8 warps and no tiles fetched ahead, fp32 prefill of 8192 tokens at 16/48
+// heads took 2.35 ms against 1.36); the second what that
+// leaves, of which the tensor core takes 11 of 12 bits, with a sum of its own (dl), because a
+// tensor core cuts what an addition shifts out: one cut a step on d instead of three.  A NaN stays in the second.
 template <bool EX>
 __device__ __forceinline__ uint32_t first_term(float x) {
   return EX ? __float_as_uint(x) : (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
 }
 template <bool EXA, bool EXB>
-__device__ __forceinline__ void mma_split(float *d, const float *a, const float *b) {
+__device__ __forceinline__ void mma_split(float *d, float *dl, const float *a, const float *b) {
   uint32_t ah[4], bh[2];
 #pragma unroll
   for (int i = 0; i < 4; ++i) ah[i] = first_term<EXA>(a[i]);
@@ -184,12 +186,12 @@ __device__ __forceinline__ void mma_split(float *d, const float *a, const float 
   for (int i = 0; i < 2; ++i) bh[i] = first_term<EXB>(b[i]);
   if (!EXB) {
     const uint32_t bl[2] = {__float_as_uint(b[0] - __uint_as_float(bh[0])), __float_as_uint(b[1] - __uint_as_float(bh[1]))};
-    mma_tf32_16x8x8(d, ah, bl);
+    mma_tf32_16x8x8(dl, ah, bl);
   }
   if (!EXA) {
     const uint32_t al[4] = {__float_as_uint(a[0] - __uint_as_float(ah[0])), __float_as_uint(a[1] - __uint_as_float(ah[1])),
                             __float_as_uint(a[2] - __uint_as_float(ah[2])), __float_as_uint(a[3] - __uint_as_float(ah[3]))};
-    mma_tf32_16x8x8(d, al, bh);
+    mma_tf32_16x8x8(dl, al, bh);
   }
   mma_tf32_16x8x8(d, ah, bh);
 }
@@ -309,6 +311,7 @@ __global__ void __launch_bounds__(NTHREADS) scan_kernel(const Scan p) {
     if (OUT) {
       // P, rows t of tile mt, columns s of quarter nq; A X^T beside it
       float acc[2][4] = {}, oi[2][4] = {}, oa[2][4] = {};
+      float accl[2][4] = {}, oil[2][4] = {}, oal[2][4] = {};
 #pragma unroll 4
       for (int k = 0; k < DA; k += 8) {
         const float af[4] = {s.a[16 * mt + gid][k + tig], s.a[16 * mt + gid + 8][k + tig],
@@ -317,9 +320,9 @@ __global__ void __launch_bounds__(NTHREADS) scan_kernel(const Scan p) {
         for (int n = 0; n < 2; ++n) {
           const int col = 8 * (2 * nq + n) + gid;
           const float bf[2] = {s.b[col][k + tig], s.b[col][k + tig + 4]};
-          mma_split<EX, EX>(acc[n], af, bf);
+          mma_split<EX, EX>(acc[n], accl[n], af, bf);
           const float xf[2] = {s.X[col][k + tig], s.X[col][k + tig + 4]};
-          mma_split<EX, false>(oi[n], af, xf);
+          mma_split<EX, false>(oi[n], oil[n], af, xf);
         }
       }
 #pragma unroll
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(NTHREADS) scan_kernel(const Scan p) {
         for (int e = 0; e < 4; ++e) {
           const int t = 16 * mt + gid + 8 * (e >> 1), sc = 8 * (2 * nq + n) + 2 * tig + (e & 1);
           const int d = p.back ? sc - t : t - sc;
-          s.P[t][sc] = d >= 0 ? acc[n][e] * s.pw[d] : 0.f;
+          s.P[t][sc] = d >= 0 ? (acc[n][e] + accl[n][e]) * s.pw[d] : 0.f;
         }
       __syncthreads();
 #pragma unroll 4
@@ -339,7 +342,7 @@ __global__ void __launch_bounds__(NTHREADS) scan_kernel(const Scan p) {
         for (int n = 0; n < 2; ++n) {
           const int dc = 8 * (2 * nq + n) + gid;
           const float bf[2] = {s.c[k + tig][dc], s.c[k + tig + 4][dc]};
-          mma_split<false, EX>(oa[n], af, bf);
+          mma_split<false, EX>(oa[n], oal[n], af, bf);
         }
       }
       TO *out = static_cast<TO *>(p.out);
@@ -353,14 +356,15 @@ __global__ void __launch_bounds__(NTHREADS) scan_kernel(const Scan p) {
           TO *o = out + ((size_t)(t0 + t) * p.Hv + w.h) * p.Dc + dc0 + 8 * (2 * nq + n) + 2 * tig;
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            o[e] = from_f32<TO>(fmaf(wi, oi[n][2 * r + e], p.s_intra * oa[n][2 * r + e]));
+            o[e] = from_f32<TO>(fmaf(wi, oi[n][2 * r + e] + oil[n][2 * r + e],
+                                     p.s_intra * (oa[n][2 * r + e] + oal[n][2 * r + e])));
         }
       }
     }
     // X <- lam^len X + sum_t (s_upd lam^{rest} c_t) b_t^T
     // (the chunk's sum on its own: tensor cores cut what an addition shifts out, which
     // over many additions to a large X would be a drift)
-    float dx[NX][4] = {};
+    float dx[NX][4] = {}, dxl[NX][4] = {};
 #pragma unroll 4
     for (int k = 0; k < C; k += 8) {
       float wt[2];
@@ -375,14 +379,14 @@ __global__ void __launch_bounds__(NTHREADS) scan_kernel(const Scan p) {
       for (int n = 0; n < NX; ++n) {
         const int da = 8 * (nq * NX + n) + gid;
         const float bf[2] = {s.b[k + tig][da], s.b[k + tig + 4][da]};
-        mma_split<false, EX>(dx[n], af, bf);
+        mma_split<false, EX>(dx[n], dxl[n], af, bf);
       }
     }
     const float lx = s.pw[len - skip];
 #pragma unroll
     for (int n = 0; n < NX; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) X[n][e] = fmaf(lx, X[n][e], dx[n][e]);
+      for (int e = 0; e < 4; ++e) X[n][e] = fmaf(lx, X[n][e], dx[n][e] + dxl[n][e]);
     if (OUT) put_x();  // (its readers have passed the barrier after P)
   }
   const bool fin = OUT && w.first && w.last && p.xf;
