@@ -38,10 +38,10 @@ linear_decode_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *
   constexpr int BATCH = GROUPS < 4 ? GROUPS : 4;
   constexpr int MT = ONE ? 1 : kMaxLinearTokens;
   const int Tn = ONE ? 1 : Tn_;
-  __shared__ __align__(16) float ks[MT][DK], qs[MT][DK];  // in lane order
-  __shared__ float vs[MT][DV];
-  __shared__ float os[MT][DV];    // the tokens' own part of o
-  __shared__ float qk[MT][MT];    // lam^{t-s} (k_s . q_t)
+  __shared__ __align__(16) float ks[MT][DK + 4], qs[MT][DK + 4];  // in lane order
+  __shared__ __align__(16) float vs[MT][DV];
+  __shared__ float os[MT][DV];                  // the tokens' own part of o
+  __shared__ __align__(16) float qk[MT][16];    // [s][t]: lam^{t-s} (k_s . q_t)
   __shared__ float lp[MT + 1];    // lam^i
 
   const int b = blockIdx.x / Hv, h = blockIdx.x - b * Hv;
@@ -64,40 +64,57 @@ linear_decode_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *
   for (int x = 0; x < BATCH; ++x) L::load(raw[x], Sin + (size_t)(x * 4 + rr) * DK, c8);
 
   const float gh = fmaxf(g[h], rows::kDecayFloor);
-  for (int x = tid; x < Tn * DK; x += 128) {
-    const int t = x / DK, d = x - t * DK;
+#pragma unroll 2
+  for (int x = tid; x < Tn * (DK / 8); x += 128) {
+    const int t = x / (DK / 8), d = 8 * (x - t * (DK / 8));
     const size_t off = (((size_t)b * Tn + t) * Hqk + j) * DK + d;
-    ks[t][L::pos(d)] = to_f32(k[off]);
-    qs[t][L::pos(d)] = to_f32(q[off]);
+    float y[8], z[8];
+    rows::load8(k + off, y);
+    rows::load8(q + off, z);
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+      *reinterpret_cast<float4 *>(&ks[t][L::pos(d + e)]) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+      *reinterpret_cast<float4 *>(&qs[t][L::pos(d + e)]) = make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
+    }
   }
-  for (int x = tid; x < Tn * DV; x += 128) {
-    const int t = x / DV, d = x - t * DV;
-    vs[t][d] = to_f32(v[(((size_t)b * Tn + t) * Hv + h) * DV + d]);
+#pragma unroll 2
+  for (int x = tid; x < Tn * (DV / 8); x += 128) {
+    const int t = x / (DV / 8), d = 8 * (x - t * (DV / 8));
+    float y[8];
+    rows::load8(v + (((size_t)b * Tn + t) * Hv + h) * DV + d, y);
+    *reinterpret_cast<float4 *>(&vs[t][d]) = make_float4(y[0], y[1], y[2], y[3]);
+    *reinterpret_cast<float4 *>(&vs[t][d + 4]) = make_float4(y[4], y[5], y[6], y[7]);
   }
   if (tid <= Tn) lp[tid] = expf(gh * (float)tid);
   __syncthreads();
-  // token x token factors, one pair per warp in turn
-  for (int x = warp; x < Tn * Tn; x += 4) {
-    const int t = x / Tn, s = x - t * Tn;
+  // token x token factors, a thread for a pair (16 lanes read one q and 16 k)
+  for (int x = tid; x < Tn * 16; x += 128) {
+    const int t = x >> 4, s = x & 15;
     if (s > t) continue;
     float a = 0.f;
-#pragma unroll
-    for (int d = lane; d < DK; d += 32) a = fmaf(ks[s][d], qs[t][d], a);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
-    if (lane == 0) qk[t][s] = a * lp[t - s];
+#pragma unroll 8
+    for (int d = 0; d < DK; d += 4) {
+      const float4 y = *reinterpret_cast<const float4 *>(&ks[s][d]), z = *reinterpret_cast<const float4 *>(&qs[t][d]);
+      a = fmaf(y.x, z.x, fmaf(y.y, z.y, fmaf(y.z, z.z, fmaf(y.w, z.w, a))));
+    }
+    qk[s][t] = a * lp[t - s];
   }
   __syncthreads();
-  for (int x = tid; x < Tn * DV; x += 128) {
-    const int t = x / DV, d = x - t * DV;
-    float a = 0.f;
-    for (int s = 0; s <= t; ++s) a = fmaf(qk[t][s], vs[s][d], a);
-    os[t][d] = a;
-  }
-  __syncthreads();
-  for (int x = tid; x < Tn * DV; x += 128) {  // from here vs holds lam^{Tn-1-t} v_t
-    const int t = x / DV, d = x - t * DV;
-    vs[t][d] *= lp[Tn - 1 - t];
+  // each column's own part of every token's output, then vs <- lam^{Tn-1-t} v_t
+  if (tid < DV) {
+    float a[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) a[t] = 0.f;
+    for (int s = 0; s < Tn; ++s) {
+      const float y = vs[s][tid];
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+        if (t >= s) a[t] = fmaf(qk[s][t], y, a[t]);  // (rows past Tn are not used)
+      vs[s][tid] = y * lp[Tn - 1 - s];
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+      if (t < Tn) os[t][tid] = a[t];
   }
   __syncthreads();
 
@@ -107,60 +124,56 @@ linear_decode_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *
 #pragma unroll
       for (int x = 0; x < BATCH; ++x) L::load(raw[x], Sin + (size_t)((gb + x) * 4 + rr) * DK, c8);
     }
-    float s[BATCH][NV4 * 4];
+    float2 s[BATCH][NV4 * 2];
 #pragma unroll
-    for (int x = 0; x < BATCH; ++x) L::widen(raw[x], s[x]);
+    for (int x = 0; x < BATCH; ++x) L::widen(raw[x], reinterpret_cast<float *>(s[x]));
     for (int t = 0; t < Tn; ++t) {
-      float p[BATCH];
+      float2 p[BATCH];
 #pragma unroll
-      for (int x = 0; x < BATCH; ++x) p[x] = 0.f;
+      for (int x = 0; x < BATCH; ++x) p[x] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int m = 0; m < NV4; ++m) {
         const float4 a = *reinterpret_cast<const float4 *>(&qs[t][32 * m + 4 * c8]);
 #pragma unroll
         for (int x = 0; x < BATCH; ++x) {
-          p[x] = fmaf(s[x][4 * m + 0], a.x, p[x]);
-          p[x] = fmaf(s[x][4 * m + 1], a.y, p[x]);
-          p[x] = fmaf(s[x][4 * m + 2], a.z, p[x]);
-          p[x] = fmaf(s[x][4 * m + 3], a.w, p[x]);
+          p[x] = __ffma2_rn(s[x][2 * m], make_float2(a.x, a.y), p[x]);
+          p[x] = __ffma2_rn(s[x][2 * m + 1], make_float2(a.z, a.w), p[x]);
         }
       }
-#pragma unroll
-      for (int off = 1; off < 8; off <<= 1)
-#pragma unroll
-        for (int x = 0; x < BATCH; ++x) p[x] += __shfl_xor_sync(0xffffffffu, p[x], off);
+      static_assert(BATCH == 4, "four row groups at a time");
+      const float sums[4] = {p[0].x + p[0].y, p[1].x + p[1].y, p[2].x + p[2].y, p[3].x + p[3].y};
+      const float px = rows::reduce4(sums, c8);
       if (c8 < BATCH) {  // lane c8 of a row group writes the row of group gb + c8
-        float px = p[0];
-#pragma unroll
-        for (int x = 1; x < BATCH; ++x) px = c8 == x ? p[x] : px;
         const int row = warp * ROWS + (gb + c8) * 4 + rr;
         o[(((size_t)b * Tn + t) * Hv + h) * DV + row] =
             from_f32<TO>(scale * fmaf(lp[t + 1], px, os[t][row]));
       }
     }
-    const float lT = lp[Tn];
+    const float2 lT = make_float2(lp[Tn], lp[Tn]);
 #pragma unroll
     for (int x = 0; x < BATCH; ++x)
 #pragma unroll
-      for (int e = 0; e < NV4 * 4; ++e) s[x][e] *= lT;
+      for (int e = 0; e < NV4 * 2; ++e) s[x][e] = __fmul2_rn(s[x][e], lT);
     for (int t = 0; t < Tn; ++t) {
-      float c[BATCH];
+      float2 c[BATCH];
 #pragma unroll
-      for (int x = 0; x < BATCH; ++x) c[x] = vs[t][warp * ROWS + (gb + x) * 4 + rr];
+      for (int x = 0; x < BATCH; ++x) {
+        const float cx = vs[t][warp * ROWS + (gb + x) * 4 + rr];
+        c[x] = make_float2(cx, cx);
+      }
 #pragma unroll
       for (int m = 0; m < NV4; ++m) {
         const float4 a = *reinterpret_cast<const float4 *>(&ks[t][32 * m + 4 * c8]);
 #pragma unroll
         for (int x = 0; x < BATCH; ++x) {
-          s[x][4 * m + 0] = fmaf(c[x], a.x, s[x][4 * m + 0]);
-          s[x][4 * m + 1] = fmaf(c[x], a.y, s[x][4 * m + 1]);
-          s[x][4 * m + 2] = fmaf(c[x], a.z, s[x][4 * m + 2]);
-          s[x][4 * m + 3] = fmaf(c[x], a.w, s[x][4 * m + 3]);
+          s[x][2 * m] = __ffma2_rn(c[x], make_float2(a.x, a.y), s[x][2 * m]);
+          s[x][2 * m + 1] = __ffma2_rn(c[x], make_float2(a.z, a.w), s[x][2 * m + 1]);
         }
       }
     }
 #pragma unroll
-    for (int x = 0; x < BATCH; ++x) L::store(Sout + (size_t)((gb + x) * 4 + rr) * DK, s[x], c8);
+    for (int x = 0; x < BATCH; ++x)
+      L::store(Sout + (size_t)((gb + x) * 4 + rr) * DK, reinterpret_cast<const float *>(s[x]), c8);
   }
 }
 

@@ -20,6 +20,16 @@ namespace rows {
 // fp32 sum, so that its powers are defined at lam = 0 too (0 * -inf is not).
 constexpr float kDecayFloor = -30.f;
 
+// Four rows' sums over the 8 lanes of a row group, each lane c8 left with the sum of
+// row c8 mod 4 (two rows change places at each of two steps: 4 shuffles, not 12).
+__device__ __forceinline__ float reduce4(const float p[4], int c8) {
+  const bool b0 = c8 & 1, b1 = c8 & 2;
+  const float a = (b0 ? p[1] : p[0]) + __shfl_xor_sync(0xffffffffu, b0 ? p[0] : p[1], 1);
+  const float b = (b0 ? p[3] : p[2]) + __shfl_xor_sync(0xffffffffu, b0 ? p[2] : p[3], 1);
+  const float c = (b1 ? b : a) + __shfl_xor_sync(0xffffffffu, b1 ? a : b, 2);
+  return c + __shfl_xor_sync(0xffffffffu, c, 4);
+}
+
 template <typename ST, int DK>
 struct Lane;
 
@@ -81,6 +91,21 @@ struct Lane<__nv_bfloat16, DK> {
     }
   }
 };
+
+// 8 consecutive elements as fp32 (16-byte aligned; fp32: 32 bytes).
+__device__ __forceinline__ void load8(const float *p, float out[8]) {
+  load4(p, out);
+  load4(p + 4, out + 4);
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float out[8]) {
+  const uint4 x = *reinterpret_cast<const uint4 *>(p);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    out[2 * e] = __uint_as_float(w[e] << 16);
+    out[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+  }
+}
 
 // Call f(ST{}, DK, DV) with the state's element type and the head dims as
 // integral constants (64 or 128 each).

@@ -436,7 +436,7 @@ tree_commit_kernel(const CommitParams p) {
   using L = rows::Lane<ST, DK>;
   constexpr int NV4 = L::NV4, ROWS = DV / 4, GROUPS = ROWS / 4, BATCH = GROUPS < 4 ? GROUPS : 4;
   extern __shared__ __align__(16) float stage[];  // k [M][DK] in lane order, v [M][DV], along the path
-  __shared__ int path[kMaxNodes];
+  __shared__ int path[kMaxNodes], par[kMaxNodes];
   __shared__ int len_s;
   __shared__ float al[kMaxNodes], bt[kMaxNodes];
   const int b = blockIdx.x / p.Hv, h = blockIdx.x - b * p.Hv;
@@ -457,12 +457,15 @@ tree_commit_kernel(const CommitParams p) {
 #pragma unroll
   for (int x = 0; x < BATCH; ++x) L::load(raw[x], Sin + (size_t)(x * 4 + rr) * DK, c8);
 
+  const int accept = p.accept[b];
+  for (int i = tid; i < M; i += 128) par[i] = p.parent[(size_t)b * M + i];
+  __syncthreads();
   if (tid == 0) {  // the path, last node first; parents strictly decrease, so the walk ends
-    int n = 0, a = p.accept[b];
+    int n = 0, a = accept;
     bool ok = a >= -1 && a < M;
     while (ok && a >= 0) {
       path[n++] = a;
-      const int pa = p.parent[(size_t)b * M + a];
+      const int pa = par[a];
       ok = pa >= -1 && pa < a;
       a = pa;
     }
@@ -476,14 +479,23 @@ tree_commit_kernel(const CommitParams p) {
   }
   const bool delta = p.beta != nullptr;
   float *ks = stage, *vs = stage + n * DK;
-  for (int x = tid; x < n * DK; x += 128) {
-    const int t = x / DK, d = x - t * DK;
-    ks[t * DK + L::pos(d)] =
-        to_f32(static_cast<const T *>(p.k)[(((size_t)b * M + path[n - 1 - t]) * p.Hqk + j) * DK + d]);
+#pragma unroll 2
+  for (int x = tid; x < n * (DK / 8); x += 128) {
+    const int t = x / (DK / 8), d = 8 * (x - t * (DK / 8));
+    float y[8];
+    rows::load8(static_cast<const T *>(p.k) + (((size_t)b * M + path[n - 1 - t]) * p.Hqk + j) * DK + d, y);
+#pragma unroll
+    for (int e = 0; e < 8; e += 4)
+      *reinterpret_cast<float4 *>(ks + t * DK + L::pos(d + e)) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
   }
-  for (int x = tid; x < n * DV; x += 128) {
-    const int t = x / DV, d = x - t * DV;
-    vs[x] = to_f32(static_cast<const T *>(p.v)[(((size_t)b * M + path[n - 1 - t]) * p.Hv + h) * DV + d]);
+#pragma unroll 2
+  for (int x = tid; x < n * (DV / 8); x += 128) {
+    const int t = x / (DV / 8), d = 8 * (x - t * (DV / 8));
+    float y[8];
+    rows::load8(static_cast<const T *>(p.v) + (((size_t)b * M + path[n - 1 - t]) * p.Hv + h) * DV + d, y);
+#pragma unroll
+    for (int e = 0; e < 8; e += 4)
+      *reinterpret_cast<float4 *>(vs + t * DV + d + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
   }
   for (int t = tid; t < n; t += 128) {
     if (delta) {
@@ -514,40 +526,44 @@ tree_commit_kernel(const CommitParams p) {
 #pragma unroll
       for (int x = 0; x < BATCH; ++x) L::load(raw[x], Sin + (size_t)((gb + x) * 4 + rr) * DK, c8);
     }
-    float s[BATCH][NV4 * 4];
+    float2 s[BATCH][NV4 * 2];
 #pragma unroll
-    for (int x = 0; x < BATCH; ++x) L::widen(raw[x], s[x]);
+    for (int x = 0; x < BATCH; ++x) L::widen(raw[x], reinterpret_cast<float *>(s[x]));
     for (int t = 0; t < n; ++t) {
-      float kf[NV4 * 4];
+      float2 kf[NV4 * 2];
 #pragma unroll
       for (int m = 0; m < NV4; ++m)
-        *reinterpret_cast<float4 *>(kf + 4 * m) = *reinterpret_cast<const float4 *>(ks + t * DK + 32 * m + 4 * c8);
+        *reinterpret_cast<float4 *>(kf + 2 * m) = *reinterpret_cast<const float4 *>(ks + t * DK + 32 * m + 4 * c8);
       const float alpha = al[t];
+      const float2 alpha2 = make_float2(alpha, alpha);
       float c[BATCH];
 #pragma unroll
       for (int x = 0; x < BATCH; ++x) c[x] = vs[t * DV + warp * ROWS + (gb + x) * 4 + rr];
       if (delta) {
-        float u[BATCH];
+        float2 u2[BATCH];
 #pragma unroll
         for (int x = 0; x < BATCH; ++x) {
-          u[x] = 0.f;
+          u2[x] = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int e = 0; e < NV4 * 4; ++e) u[x] = fmaf(s[x][e], kf[e], u[x]);
+          for (int e = 0; e < NV4 * 2; ++e) u2[x] = __ffma2_rn(s[x][e], kf[e], u2[x]);
         }
+        static_assert(BATCH == 4, "four row groups at a time");
+        const float sums[4] = {u2[0].x + u2[0].y, u2[1].x + u2[1].y, u2[2].x + u2[2].y, u2[3].x + u2[3].y};
+        const float mine = rows::reduce4(sums, c8);  // of row group c8 mod 4
 #pragma unroll
-        for (int off = 1; off < 8; off <<= 1)
-#pragma unroll
-          for (int x = 0; x < BATCH; ++x) u[x] += __shfl_xor_sync(0xffffffffu, u[x], off);
-#pragma unroll
-        for (int x = 0; x < BATCH; ++x) c[x] = bt[t] * (c[x] - alpha * u[x]);
+        for (int x = 0; x < BATCH; ++x)
+          c[x] = bt[t] * (c[x] - alpha * __shfl_sync(0xffffffffu, mine, (lane & ~7) | x));
       }
 #pragma unroll
-      for (int x = 0; x < BATCH; ++x)
+      for (int x = 0; x < BATCH; ++x) {
+        const float2 c2 = make_float2(c[x], c[x]);
 #pragma unroll
-        for (int e = 0; e < NV4 * 4; ++e) s[x][e] = fmaf(alpha, s[x][e], c[x] * kf[e]);
+        for (int e = 0; e < NV4 * 2; ++e) s[x][e] = __ffma2_rn(alpha2, s[x][e], __fmul2_rn(c2, kf[e]));
+      }
     }
 #pragma unroll
-    for (int x = 0; x < BATCH; ++x) L::store(Sout + (size_t)((gb + x) * 4 + rr) * DK, s[x], c8);
+    for (int x = 0; x < BATCH; ++x)
+      L::store(Sout + (size_t)((gb + x) * 4 + rr) * DK, reinterpret_cast<const float *>(s[x]), c8);
   }
 }
 
