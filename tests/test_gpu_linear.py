@@ -305,3 +305,78 @@ def test_graph_and_streams(D):
     torch.cuda.synchronize()
     for a, b, c, d in zip(eager, aside, graphed, again):
         assert torch.equal(a, b) and torch.equal(a, c) and torch.equal(a, d)
+
+
+@pytest.mark.parametrize("Hqk,Hv", [(1, 3), (2, 2)])
+@pytest.mark.parametrize("n", [700, 2300])
+def test_gradients_of_a_sequence_do_not_depend_on_its_neighbours(Hqk, Hv, n):
+    """The values of the sequences before and after are not finite; bit for bit."""
+    x, _, S0, r = make([n], Hqk, Hv, 128, 128, "bf16", seed=33)
+    do, dsf = r(n, Hv, 128).to(torch.bfloat16), r(1, Hv, 128, 128)
+    one = api.linear_prefill_backward(*dev(x["q"], x["k"], x["v"], x["g"], do), initial_state=S0.to(DEV),
+                                      d_final_state=dsf.to(DEV))
+    wide = [torch.cat([torch.full_like(t[:77], float("nan")), t, torch.full_like(t[:200], float("inf"))])
+            for t in (x["q"], x["k"], x["v"], do)]
+    cut = torch.tensor([0, 77, 77 + n, 277 + n], dtype=torch.int32, device=DEV)
+    three = lambda t: t.expand(3, *t.shape[1:]).contiguous()  # noqa: E731
+    # (as many tokens as cut the sequence the same way: its share of a multiprocessor is rounded to chunks)
+    many = api.linear_prefill_backward(*dev(*wide[:3], x["g"], wide[3]), cu_seqlens=cut,
+                                       initial_state=three(S0).to(DEV), d_final_state=three(dsf).to(DEV))
+    torch.cuda.synchronize()
+    for name, a, b in zip(("dq", "dk", "dv"), one, many):
+        b = b[77:77 + n]
+        assert torch.isfinite(b).all(), name
+        if n < 1000:
+            assert torch.equal(a, b), name
+        else:  # cut at other places: the roundings of the operands differ
+            assert float((a.float() - b.float()).norm() / a.float().norm()) <= R.UB16, name
+    assert torch.isfinite(many[3][1]).all()
+
+
+def test_largest_pool_offsets():
+    """A slot whose byte offset passes 32 bits (fp32 pool of 2,200 slots of 2 MB)."""
+    Hv, D, slots = 32, 128, 2200
+    x, _, _, r = make([2], 1, Hv, D, D, "bf16", seed=35)
+    pool = torch.zeros(slots, Hv, D, D, device=DEV)
+    last = r(Hv, D, D)
+    pool[-1].copy_(last.to(DEV))
+    src = torch.tensor([slots - 1], dtype=torch.int32, device=DEV)
+    q, k, v, g = dev(x["q"], x["k"], x["v"], x["g"])
+    par = torch.tensor([[-1, 0]], dtype=torch.int32, device=DEV)
+    ot = api.decode_tree(q[None], k[None], v[None], g, None, par, pool, src_slot=src)
+    o = api.linear_decode_tokens(q[None], k[None], v[None], g, pool, src_slot=src)
+    torch.cuda.synchronize()
+    ref, om, S, Sm, _ = R.tree(x["q"], x["k"], x["v"], x["g"], None, [-1, 0], last)
+    R.check(ot[0], ref, om, R.gamma(D, 2, 2.0 ** -22, 18), "tree", R.U32)
+    R.check(o[0], ref, om, R.gamma(D, 2), "decode", R.U32)
+    R.check(pool[-1], S[1], Sm[1], R.gamma(1, 2), "state", R.U32)
+    assert not pool[:-1].any()
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, each with its own workspace and outputs."""
+    L = [2500, 40]
+    x, cu, S0, r = make(L, 4, 8, 128, 128, "bf16", seed=37)
+    do = r(sum(L), 8, 128).to(torch.bfloat16).to(DEV)
+    cut = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    a, s0 = dev(x["q"], x["k"], x["v"], x["g"]), S0.to(DEV)
+    size = lambda b: api.linear_prefill_workspace_size(2, sum(L), 4, 8, 128, 128, torch.bfloat16, b)  # noqa: E731
+
+    def calls(ws, wb):
+        return [*api.linear_prefill(*a, cu_seqlens=cut, initial_state=s0, o_dtype=torch.bfloat16, workspace=ws),
+                *api.linear_prefill_backward(*a, do, cu_seqlens=cut, initial_state=s0, d_final_state=s0, workspace=wb)]
+
+    spaces = [[torch.zeros(size(b), dtype=torch.uint8, device=DEV) for b in (False, True)] for _ in range(2)]
+    want = calls(*spaces[0])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(DEV) for _ in range(2)]
+    for _ in range(4):
+        got = []
+        for st, sp in zip(streams, spaces):
+            with torch.cuda.stream(st):
+                got.append(calls(*sp))
+        torch.cuda.synchronize()
+        for g in got:
+            for u, v in zip(want, g):
+                assert torch.equal(u, v)
+    assert all(api.get_device_status(w) == api.GDN_OK for sp in spaces for w in sp)
