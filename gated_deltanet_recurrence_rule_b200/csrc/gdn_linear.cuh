@@ -41,7 +41,7 @@ struct Scan {
   const int4 *units;         // [segments] the segments, longest first (below); NULL where each
                              // sequence is one segment
   int L;
-  float *seg_state;          // [segments, Hv, Dc, Da] added (states only) or starting state;
+  float *seg_state;          // [cut segments, Hv, Dc, Da] added (states only) or starting state;
                              // a sequence of one segment starts from x0 (and x0 may be xf: of
                              // several, the last may end before the first has started)
   const void *x0;            // [N, Hv, Dc, Da], or (x0_tr) [N, Hv, Da, Dc]; NULL: zeros
@@ -56,8 +56,9 @@ struct Unit {
   int first, last;  // the segment its sequence's scan starts, ends with
 };
 
-// A segment of the plan: x its number, with kFirst and kLast where it is the first or
-// last of its sequence (-1: no segment), y the sequence, z and w its tokens.
+// A segment of the plan: x the slot of its state (of a sequence of several), with kFirst
+// and kLast where it is the first or last of its sequence (-1: no segment), y the
+// sequence, z and w its tokens.
 constexpr int kFirst = 1 << 30, kLast = 1 << 29;
 
 // False where unit `u` does not exist or cu_seqlens is inconsistent.

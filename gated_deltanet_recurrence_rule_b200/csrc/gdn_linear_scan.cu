@@ -15,15 +15,20 @@ using chunk::mma_tf32_16x8x8;
 
 // ---------------------------------------------------------------- plan
 // The segments of the packed sequences (an empty one has one, of no tokens), by one
-// CTA.  Units of unequal length are started longest first, so that the last ones to
-// finish are short; beyond kMaxSorted segments there are enough waves of units for the
-// order not to matter.  Entries past the last segment, and all of them where cu_seqlens
-// is inconsistent, are marked.
+// CTA: `units` all of them, `cuts` the sequences of several (x the sequence, y the slot
+// of the first segment's state, z how many, w the tokens) and `cut_units` their
+// segments, which alone take part in (1) and (2).  Units of unequal length are started
+// longest first, so that the last ones to finish are short; beyond kMaxSorted segments
+// there are enough waves of units for the order not to matter.  Entries past the last
+// of a table, and all of them where cu_seqlens is inconsistent, are marked.
+struct Plan {
+  int4 *units, *cut_units, *cuts;
+  int max_seg, max_cut_seg, max_cut;  // entries of the tables
+};
 constexpr int kMaxSorted = 512;
 __global__ void __launch_bounds__(1024)
-plan_segments_kernel(const int32_t *__restrict__ cu, int N, int T, int L, int max_seg, int32_t *first_seg,
-                     int4 *units, int32_t *status) {
-  __shared__ int wsum[32], run_s;
+plan_segments_kernel(const int32_t *__restrict__ cu, int N, int T, int L, const Plan p, int32_t *status) {
+  __shared__ int wsum[32], wcut[32], run_s, run_c, cuts_s;
   __shared__ int4 table[kMaxSorted];
   pdl_wait();  // nothing is read before the previous kernel on the stream is done
   pdl_allow_next();
@@ -33,55 +38,62 @@ plan_segments_kernel(const int32_t *__restrict__ cu, int N, int T, int L, int ma
     const int c = cu[i];
     bad |= c < 0 || c > T || (i == 0 && c != 0) || (i == N && c != T) || (i < N && cu[i + 1] < c);
   }
-  if (tid == 0) run_s = 0;
-  if (__syncthreads_or(bad)) {
-    if (tid == 0) {
-      report_status(status, GDN_ERR_BAD_SEQLENS);
-      first_seg[N] = -1;
+  if (tid == 0) run_s = run_c = cuts_s = 0;
+  bad = __syncthreads_or(bad);
+  if (bad && tid == 0) report_status(status, GDN_ERR_BAD_SEQLENS);
+  auto scan = [&](int x) {  // inclusive, of a warp
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
     }
-    for (int i = tid; i < max_seg; i += 1024) units[i].x = -1;
-    return;
-  }
-  for (int base = 0; base < N; base += 1024) {
+    return x;
+  };
+  for (int base = 0; base < (bad ? 0 : N); base += 1024) {
     const int n = base + tid;
     const int c0 = n < N ? cu[n] : 0, c1 = n < N ? cu[n + 1] : 0;
     const int cnt = n < N ? max(1, (int)(((long long)c1 - c0 + L - 1) / L)) : 0;
-    int inc = cnt;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, inc, off);
-      if (lane >= off) inc += x;
+    const int cut = cnt > 1 ? cnt : 0;
+    const int inc = scan(cnt), inc_cut = scan(cut);
+    if (lane == 31) {
+      wsum[wid] = inc;
+      wcut[wid] = inc_cut;
     }
-    if (lane == 31) wsum[wid] = inc;
     __syncthreads();
     if (wid == 0) {
-      int v = wsum[lane];
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, v, off);
-        if (lane >= off) v += x;
-      }
-      wsum[lane] = v;
+      wsum[lane] = scan(wsum[lane]);
+      wcut[lane] = scan(wcut[lane]);
     }
     __syncthreads();
     const int start = run_s + (wid ? wsum[wid - 1] : 0) + inc - cnt;
-    if (n < N) {
-      first_seg[n] = start;
-      for (int i = 0; i < cnt; ++i) {
-        const int sg = start + i;
-        const int4 s = make_int4(sg | (i == 0 ? kFirst : 0) | (i == cnt - 1 ? kLast : 0), n, c0 + i * L,
-                                 i == cnt - 1 ? c1 : c0 + (i + 1) * L);
-        units[sg] = s;
-        if (sg < kMaxSorted) table[sg] = s;
-      }
+    const int slot = run_c + (wid ? wcut[wid - 1] : 0) + inc_cut - cut;
+    auto put = [&](int n, int c0, int c1, int i, int cnt, int sg, int slot) {
+      const int4 s = make_int4(slot | (i == 0 ? kFirst : 0) | (i == cnt - 1 ? kLast : 0), n, c0 + i * L,
+                               i == cnt - 1 ? c1 : c0 + (i + 1) * L);
+      p.units[sg] = s;
+      if (sg < kMaxSorted) table[sg] = s;
+      if (cnt > 1) p.cut_units[slot] = s;
+    };
+    if (cnt == 1) put(n, c0, c1, 0, 1, start, 0);
+    if (cut) p.cuts[atomicAdd(&cuts_s, 1)] = make_int4(n, slot, cnt, c1 - c0);
+    for (unsigned m = __ballot_sync(0xffffffffu, cut); m; m &= m - 1) {  // the segments of one, by its warp
+      const int src = __ffs(m) - 1;
+      const int b0 = __shfl_sync(0xffffffffu, c0, src), b1 = __shfl_sync(0xffffffffu, c1, src);
+      const int segs = __shfl_sync(0xffffffffu, cut, src), sg = __shfl_sync(0xffffffffu, start, src);
+      const int sl = __shfl_sync(0xffffffffu, slot, src);
+      for (int i = lane; i < segs; i += 32) put(n - lane + src, b0, b1, i, segs, sg + i, sl + i);
     }
     __syncthreads();
-    if (tid == 0) run_s += wsum[31];
+    if (tid == 0) {
+      run_s += wsum[31];
+      run_c += wcut[31];
+    }
     __syncthreads();
   }
   const int total = run_s;
-  if (tid == 0) first_seg[N] = total;
-  for (int i = total + tid; i < max_seg; i += 1024) units[i].x = -1;
+  for (int i = total + tid; i < p.max_seg; i += 1024) p.units[i].x = -1;
+  for (int i = run_c + tid; i < p.max_cut_seg; i += 1024) p.cut_units[i].x = -1;
+  for (int i = cuts_s + tid; i < p.max_cut; i += 1024) p.cuts[i].x = -1;
   if (total <= kMaxSorted && tid < total) {
     const int len = table[tid].w - table[tid].z;
     int rank = 0;
@@ -89,7 +101,7 @@ plan_segments_kernel(const int32_t *__restrict__ cu, int N, int T, int L, int ma
       const int other = table[i].w - table[i].z;
       rank += other > len || (other == len && i < tid);
     }
-    units[rank] = table[tid];
+    p.units[rank] = table[tid];
   }
 }
 
@@ -100,8 +112,8 @@ plan_segments_kernel(const int32_t *__restrict__ cu, int N, int T, int L, int ma
 // elements a thread, four segments' loads in flight.
 struct Prefix {
   const float *g;
-  const int32_t *cu, *first_seg;
-  int N, Hv, L, Da, Dc, back;
+  const int4 *cuts;  // of the plan
+  int Hv, L, Da, Dc, back;
   float *nat, *tr;
   int keep_nat;      // the starting states are wanted in nat
   const void *x0;    // [N, Hv, Dc, Da]
@@ -115,11 +127,11 @@ __global__ void __launch_bounds__(256) prefix_kernel(const Prefix p) {
   pdl_allow_next();
   const int tiles = (p.Da / 32) * (p.Dc / 32);
   const int unit = blockIdx.x / tiles, tl = blockIdx.x - unit * tiles;
-  const int n = unit / p.Hv, h = unit - n * p.Hv;
-  const int total = p.first_seg[p.N], s0 = p.first_seg[n], s1 = p.first_seg[n + 1];
-  const int len = p.cu[n + 1] - p.cu[n], cnt = s1 - s0;
+  const int ci = unit / p.Hv, h = unit - ci * p.Hv;
+  const int4 seq = p.cuts[ci];
+  const int n = seq.x, s0 = seq.y, cnt = seq.z, len = seq.w;
   const float gh = fmaxf(p.g[h], -30.f);
-  if (total < 0 || cnt < 2) return;  // inconsistent cu_seqlens; one segment
+  if (n < 0) return;
   const int i0 = 32 * (tl / (p.Da / 32)), j0 = 32 * (tl % (p.Da / 32));
   const int r = threadIdx.x >> 3, c = 4 * (threadIdx.x & 7);
   const size_t in_state = (size_t)(i0 + r) * p.Da + j0 + c;
@@ -453,41 +465,53 @@ namespace {
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// Segment length in tokens.  tcgen05 form: a chunk of 128 tokens takes about 2.8 us of
-// one multiprocessor, 1.4 us more where the sequence is cut (its states), and cutting
-// costs about 27 us of launches, starts and state moves; so a sequence is cut into
-// one segment for each multiprocessor of its head's share, if that saves more than it
-// costs (prefill of 8192 tokens, 48 heads: 155 us in 3 segments, about 190 in one).
-// The other form: chunks of 64 tokens take several times as long, so segments go down
-// to two chunks as long as there are multiprocessors.
-int segment_len(int64_t T, int Hv, int Dv, bool tc) {
-  if (tc) {
-    const double s = std::max(1, sm_count() / Hv);  // segments of one wave
-    const double chunks = (double)((T + 127) / 128);
-    if (chunks * (2.8 - (2.8 + 1.4) / s) <= 27.0) return (int)std::max<int64_t>(128, round_up((size_t)T, 128));
-    return (int)round_up((size_t)((T + (int64_t)s - 1) / (int64_t)s), 128);
+// Segment length in tokens.  Cutting lets the multiprocessors that a call's heads leave
+// idle work on a sequence, but its chunks then cost more (the segments' states) and
+// there are launches, starts and state moves on top; so the total's chunks are counted
+// in microseconds both ways, with costs taken from timings.  At 48 heads of 128, us for
+// one segment and for 3: tcgen05 form, 1024 tokens 41 and 44, 2048 68 and 58, 8192 223
+// and 130; its backward, 1024 tokens 135 and 118.  The other form (fp32), 256 tokens 59
+// and 94, 1024 201 and 224, 8192 1550 and 1422.  Segments for more waves than these cost
+// more again (8192 tokens in 6: 154), and so do segments of one 64-token chunk (4096
+// tokens, 4 heads, fp32: 89 us in 16 segments, 99 in 32).
+int segment_len(int64_t T, int Hv, int Dv, bool tc, bool backward) {
+  const int ch = tc ? 128 : 64, ctas = tc ? Hv : Hv * (Dv / DCT), sms = sm_count();
+  const double scans = backward ? 3 : 1, states = backward ? 2 : 1;
+  const double chunk = scans * (tc ? 3.2 : 11.8), cut = chunk + states * (tc ? 1.2 : 4.3);
+  const double fixed = tc ? (backward ? 28 : 22) : 25;
+  const int64_t n = std::max<int64_t>(1, (T + ch - 1) / ch);
+  int64_t best = n;
+  double least = chunk * (double)n;
+  for (int waves = 1; waves <= (tc ? 1 : 2); ++waves) {
+    const int64_t s = (int64_t)waves * sms / ctas;
+    if (s < 2) continue;
+    const int64_t per = std::max<int64_t>(tc ? 1 : 2, (n + s - 1) / s);
+    const double us = fixed + cut * (double)(per * waves);
+    if (us < least) {
+      least = us;
+      best = per;
+    }
   }
-  const int64_t units = std::max<int64_t>(1, 2 * sm_count() / (Hv * (Dv / DCT)));
-  return (int)std::max<int64_t>(128, round_up((size_t)((T + units - 1) / units), 64));
+  return (int)(best * ch);
 }
 
 struct Layout {
   int L;
-  int64_t max_seg;
-  size_t first_seg, units, nat, tr, part, total;
+  int64_t max_seg, max_cut, max_cut_seg;  // segments; sequences of several, and their segments
+  size_t units, nat, tr, part, total;
 };
 
 Layout layout(int64_t N, int64_t T, int Hqk, int Hv, int Dk, int Dv, bool tc, bool backward) {
   Layout l;
-  l.L = segment_len(T, Hv, Dv, tc);
+  l.L = segment_len(T, Hv, Dv, tc, backward);
   const bool one = T <= l.L;
   l.max_seg = one ? N : T / l.L + N;
+  l.max_cut = one ? 0 : std::min<int64_t>(N, T / l.L);
+  l.max_cut_seg = one ? 0 : T / l.L + l.max_cut;
   size_t at = kWorkspaceHeaderBytes;
-  l.first_seg = at;
-  if (!one) at = round_up(at + sizeof(int32_t) * (size_t)(N + 1), 256);
   l.units = at;
-  if (!one) at = round_up(at + sizeof(int4) * (size_t)l.max_seg, 1024);
-  const size_t states = one ? 0 : round_up((size_t)l.max_seg * Hv * Dk * Dv * sizeof(float), 1024);
+  if (!one) at = round_up(at + sizeof(int4) * (size_t)(l.max_seg + l.max_cut_seg + l.max_cut), 1024);
+  const size_t states = round_up((size_t)l.max_cut_seg * Hv * Dk * Dv * sizeof(float), 1024);
   l.nat = at;
   at += states;
   l.tr = at;
@@ -518,18 +542,23 @@ static cudaError_t run_scan(const Scan &p, bool tc, int units, int dtype, int ou
   return tc ? launch_scan_tc(p, units, out_dtype, stream) : launch_scan(p, units, dtype, out_dtype, stream);
 }
 
-// Plan the segments; point `p` at them and `x` at the first of each sequence.
-static cudaError_t run_plan(Scan &p, Prefix &x, const Layout &l, unsigned char *ws, cudaStream_t stream) {
-  int32_t *first_seg = reinterpret_cast<int32_t *>(ws + l.first_seg);
-  int4 *units = reinterpret_cast<int4 *>(ws + l.units);
-  p.units = units;
-  x.first_seg = first_seg;
-  return launch_pdl(plan_segments_kernel, dim3(1), dim3(1024), 0, stream, p.cu, p.N, p.T, l.L, (int)l.max_seg,
-                    first_seg, units, p.status);
+// Plan the segments of p's sequences.
+static cudaError_t run_plan(const Scan &p, const Layout &l, unsigned char *ws, Plan &plan, cudaStream_t stream) {
+  plan.units = reinterpret_cast<int4 *>(ws + l.units);
+  plan.cut_units = plan.units + l.max_seg;
+  plan.cuts = plan.cut_units + l.max_cut_seg;
+  plan.max_seg = (int)l.max_seg; plan.max_cut_seg = (int)l.max_cut_seg; plan.max_cut = (int)l.max_cut;
+  return launch_pdl(plan_segments_kernel, dim3(1), dim3(1024), 0, stream, p.cu, p.N, p.T, l.L, plan, p.status);
 }
 
-static cudaError_t run_prefix(const Prefix &p, cudaStream_t stream) {
-  const unsigned grid = (unsigned)p.N * (unsigned)p.Hv * (unsigned)((p.Da / 32) * (p.Dc / 32));
+// What the segments add to the states, into p.seg_state (p.out is NULL).
+static cudaError_t run_states(Scan p, bool tc, const Plan &plan, int dtype, cudaStream_t stream) {
+  p.units = plan.cut_units;
+  return run_scan(p, tc, plan.max_cut_seg * p.Hv, dtype, dtype, stream);
+}
+
+static cudaError_t run_prefix(const Prefix &p, const Plan &plan, cudaStream_t stream) {
+  const unsigned grid = (unsigned)plan.max_cut * (unsigned)p.Hv * (unsigned)((p.Da / 32) * (p.Dc / 32));
   return launch_pdl(prefix_kernel, dim3(grid), dim3(256), 0, stream, p);
 }
 
@@ -553,17 +582,18 @@ cudaError_t launch_linear_prefill(const void *q, const void *k, const void *v, c
     p.out = o;
     return run_scan(p, tc, N * Hv, dtype, o_dtype, stream);
   }
-  Prefix x = {};
-  cudaError_t e = run_plan(p, x, l, w, stream);
+  Plan plan;
+  cudaError_t e = run_plan(p, l, w, plan, stream);
   if (e != cudaSuccess) return e;
   p.seg_state = reinterpret_cast<float *>(w + l.nat);
-  const int units = (int)l.max_seg * Hv;
-  if ((e = run_scan(p, tc, units, dtype, dtype, stream)) != cudaSuccess) return e;  // out NULL: states
-  x.g = g; x.cu = cu; x.N = N; x.Hv = Hv; x.L = l.L; x.Da = Dk; x.Dc = Dv;
+  if ((e = run_states(p, tc, plan, dtype, stream)) != cudaSuccess) return e;
+  Prefix x = {};
+  x.g = g; x.cuts = plan.cuts; x.Hv = Hv; x.L = l.L; x.Da = Dk; x.Dc = Dv;
   x.nat = p.seg_state; x.keep_nat = 1; x.x0 = s0; x.xf = sf; x.x_bf16 = p.x_bf16;
-  if ((e = run_prefix(x, stream)) != cudaSuccess) return e;
+  if ((e = run_prefix(x, plan, stream)) != cudaSuccess) return e;
   p.out = o;
-  return run_scan(p, tc, units, dtype, o_dtype, stream);
+  p.units = plan.units;
+  return run_scan(p, tc, plan.max_seg * Hv, dtype, o_dtype, stream);
 }
 
 cudaError_t launch_linear_backward(const void *q, const void *k, const void *v, const float *g,
@@ -584,9 +614,13 @@ cudaError_t launch_linear_backward(const void *q, const void *k, const void *v, 
   float *part = reinterpret_cast<float *>(w + l.part);
   const int units = (int)l.max_seg * Hv;
   cudaError_t e = cudaSuccess;
+  Plan plan = {};
+  if (!one) {
+    if ((e = run_plan(base, l, w, plan, stream)) != cudaSuccess) return e;
+    base.units = plan.units;
+  }
   Prefix x = {};
-  if (!one && (e = run_plan(base, x, l, w, stream)) != cudaSuccess) return e;
-  x.g = g; x.cu = cu; x.N = N; x.Hv = Hv; x.L = l.L; x.Da = Dk; x.Dc = Dv;
+  x.g = g; x.cuts = plan.cuts; x.Hv = Hv; x.L = l.L; x.Da = Dk; x.Dc = Dv;
   x.nat = nat; x.tr = tr;
 
   // dq (and dk) of a query/key head: fp32 partials of its value heads, then their sum
@@ -608,9 +642,9 @@ cudaError_t launch_linear_backward(const void *q, const void *k, const void *v, 
   p.a = q; p.Ha = Hqk; p.b = k; p.Hb = Hqk; p.c = v; p.Hc = Hv; p.Da = Dk; p.Dc = Dv; p.s_upd = 1.f;
   if (!one) {
     p.seg_state = nat;
-    if ((e = run_scan(p, tc, units, dtype, dtype, stream)) != cudaSuccess) return e;
+    if ((e = run_states(p, tc, plan, dtype, stream)) != cudaSuccess) return e;
     x.x0 = s0; x.back = 0; x.keep_nat = 0;
-    if ((e = run_prefix(x, stream)) != cudaSuccess) return e;
+    if ((e = run_prefix(x, plan, stream)) != cudaSuccess) return e;
   }
   p = base;
   p.a = d_o; p.Ha = Hv; p.b = v; p.Hb = Hv; p.c = k; p.Hc = Hqk; p.Da = Dv; p.Dc = Dk;
@@ -622,9 +656,9 @@ cudaError_t launch_linear_backward(const void *q, const void *k, const void *v, 
   p.a = k; p.Ha = Hqk; p.b = q; p.Hb = Hqk; p.c = d_o; p.Hc = Hv; p.Da = Dk; p.Dc = Dv;
   p.s_intra = p.s_upd = scale; p.s_inter = 1.f; p.seg_state = nat; p.x0 = dsf; p.xf = ds0;
   if (!one) {
-    if ((e = run_scan(p, tc, units, dtype, dtype, stream)) != cudaSuccess) return e;
+    if ((e = run_states(p, tc, plan, dtype, stream)) != cudaSuccess) return e;
     x.x0 = dsf; x.back = 1; x.keep_nat = 1; x.xf = ds0;
-    if ((e = run_prefix(x, stream)) != cudaSuccess) return e;
+    if ((e = run_prefix(x, plan, stream)) != cudaSuccess) return e;
   }
   p.out = dv;
   if ((e = run_scan(p, tc, units, dtype, dtype, stream)) != cudaSuccess) return e;

@@ -429,9 +429,9 @@ int32_t gdn_prefill_backward_sequential(const void *q, const void *k, const void
  * gdn_linear_prefill_workspace_size: bytes of device workspace that
  * gdn_linear_prefill (backward = 0) or gdn_linear_prefill_backward (1) needs (0
  * for invalid sizes): the status header, and for inputs longer than one
- * multiprocessor's share the segment tables and one starting state per (segment,
- * value head); for the backward also the transposed states and, where Hv > Hqk,
- * an fp32 [T, Hv, Dk] buffer of per-value-head dq or dk.
+ * multiprocessor's share the segment tables and one starting state per (segment of a
+ * sequence longer than that share, value head); for the backward also the transposed
+ * states and, where Hv > Hqk, an fp32 [T, Hv, Dk] buffer of per-value-head dq or dk.
  */
 size_t gdn_linear_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens,
                                          int32_t num_qk_heads, int32_t num_v_heads,
@@ -451,6 +451,13 @@ size_t gdn_linear_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens,
  * itself rounded to bf16.  Everything else runs on warp-level tf32 MMAs with split
  * operands, at about fp32 accuracy.  Rows past a sequence's end are neither read
  * into its results nor written.
+ *
+ * g is <= 0 (a decay), and one below -30 is taken as -30.  A token that is not finite
+ * may reach the outputs of its whole chunk (128 tokens of its sequence on the tensor
+ * cores, 64 otherwise), earlier ones included, as well as all later ones; never those
+ * of another sequence.  How a sequence is cut into segments depends on total_tokens,
+ * and the order of its sums with it: the same sequence packed with others can differ
+ * in rounding from its result alone.
  */
 int32_t gdn_linear_prefill(const void *q, const void *k, const void *v, const float *g,
                            const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,

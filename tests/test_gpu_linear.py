@@ -380,3 +380,28 @@ def test_two_streams_at_once():
             for u, v in zip(want, g):
                 assert torch.equal(u, v)
     assert all(api.get_device_status(w) == api.GDN_OK for sp in spaces for w in sp)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_cut_sequences_among_many(dtype):
+    """Over a thousand sequences, a few of them long enough to be cut into segments:
+    outputs, final states, and the gradients that pass through the states."""
+    L = [i % 4 for i in range(1200)]
+    for i, n in ((10, 900), (500, 1700), (501, 700), (1030, 333), (1199, 1100)):
+        L[i] = n
+    x, cu, S0, r = make(L, 1, 2, 64, 64, dtype, seed=43)
+    do, dsf = r(sum(L), 2, 64).to(DT[dtype]), r(len(L), 2, 64, 64) * 0.5
+    args = dev(x["q"], x["k"], x["v"], x["g"])
+    cut = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    o, f = api.linear_prefill(*args, cu_seqlens=cut, initial_state=S0.to(DEV), o_dtype=DT[dtype])
+    dq, dk, dv, ds0 = api.linear_prefill_backward(*args, do.to(DEV), cu_seqlens=cut, initial_state=S0.to(DEV),
+                                                  d_final_state=dsf.to(DEV))
+    torch.cuda.synchronize()
+    ref, om, F, Fm = R.scan(x["q"], x["k"], x["v"], x["g"], cu, S0)
+    R.check(f, F, Fm, rel32(L, 64), "final state", R.U32)
+    stored = R.UB16 if dtype == "bf16" else R.U32
+    R.check(o, ref, om, 2 * R.UB16 if dtype == "bf16" else rel32(L, 64), "o", stored)
+    tol = rel32(L, 64) + 2 * R.U32
+    for got, w, m, name in zip((dq, dk, dv, ds0), *grads_ref(x, cu, S0, do, dsf, 1.0), ("dq", "dk", "dv", "dS0")):
+        exact = dtype == "fp32" or name == "dS0"
+        R.check(got, w, m, tol if exact else 2 * R.UB16, name, R.U32 if exact else R.UB16)
