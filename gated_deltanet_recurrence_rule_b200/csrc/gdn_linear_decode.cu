@@ -14,6 +14,9 @@
 // One 128-thread CTA per (b, h), 8 lanes per row, lane c8 of a row holding
 // float4 pieces so that a warp's load covers four whole 128-byte segments;
 // four row groups (16 rows of a warp) are in flight before the first is used.
+// Measured, 16/48 heads of 128, fp32 states in place: 64 sequences x 1 token 63.9 us
+// (403 MB, 6.3 TB/s, 97 % of the copy bandwidth), x 4 81 us, x 16 166 us, where the
+// fp32 pipe binds; bf16 states 38 us for one token.
 #include "gdn_common.cuh"
 #include "gdn_rows.cuh"
 
@@ -197,6 +200,9 @@ cudaError_t launch_linear_decode(const void *q, const void *k, const void *v, co
                           static_cast<ST *>(state_out), src_slot, dst_slot, num_slots,
                           static_cast<TO *>(o), Tn, Hqk, Hv, scale, status);
       };
+      // One token has no token x token part and no loop over tokens: from a flushed L2, 64
+      // sequences take 71.7 us against 73.7 for the general kernel, with bf16 states 41.0
+      // against 45.1, one sequence 10.2 against 12.3.
       if (Tn == 1) return go(linear_decode_kernel<T, TO, ST, DK, DV, true>);
       return go(linear_decode_kernel<T, TO, ST, DK, DV, false>);
     });

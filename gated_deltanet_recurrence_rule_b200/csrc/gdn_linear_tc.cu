@@ -9,15 +9,24 @@
 //     dX = (w C)^T B                 w_t = s_upd lam^{rest}
 //     out_t = s_inter lam^{p+1} Oi_t + s_intra Oa_t,   X <- lam^len X + dX.
 // A head dim of 64 runs on the same tiles: TMA fills the columns past it with zeros and
-// does not store them.  (The products are then up to four times what is needed, but
-// the loads, stores and elementwise work bound the kernel: 8192 tokens at 16/48 heads
-// take as long as the halved bytes allow less about a tenth.)
+// does not store them.  (The products are then up to four times what is needed, and the
+// halved bytes buy little: 8192 tokens at 16/48 heads take 120 us against 130.)
 // Precision.  A, B, C are exact bf16.  The state is fp32 in registers; w C enters dX
 // as bf16 terms cut from its fp32 value, 8 bits each: three (all 24 bits) where the
 // state is returned or handed to another segment, two where it only serves outputs;
 // each chunk's dX is summed apart and added once, rounded to nearest.  P . lam^{..}
 // and X are rounded to bf16 once as operands of the output, whose own rounding to
 // bf16 is as large.
+//
+// Bound and measured (8192 tokens, 16/48 heads of 128).  The outputs kernel takes 76 us
+// at 243 MB of HBM traffic, 3.0 TB/s, with the tensor pipe active 39 % of the time: the
+// products read two 32 KB operands from shared memory each, which every chunk's loads,
+// X, P and output tiles pass through as well, about 5,600 cycles a chunk of that against
+// 3,700 for the chunk's share of HBM.  The states kernel takes 40 us.  The whole prefill
+// takes 130 us by itself and 140 in a loop of many, where the board is at its power limit
+// (980 W) and the clock falls to 1.67 GHz; a packed batch of 65,000 tokens 664 and 770 (1.53
+// GHz).  A batch of 256 prompts of 100 tokens takes 897 us: one CTA per (prompt, head),
+// 10.8 us each, whose start and end do not overlap with another's.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

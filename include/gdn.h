@@ -452,8 +452,7 @@ size_t gdn_linear_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens,
  * operands, at about fp32 accuracy.  Rows past a sequence's end are neither read
  * into its results nor written.
  *
- * g is <= 0 (a decay), and one below -30 is taken as -30.  A token that is not finite
- * may reach the outputs of its whole chunk (128 tokens of its sequence on the tensor
+ * A token that is not finite may reach the outputs of its whole chunk (128 tokens of its sequence on the tensor
  * cores, 64 otherwise), earlier ones included, as well as all later ones; never those
  * of another sequence.  How a sequence is cut into segments depends on total_tokens,
  * and the order of its sums with it: the same sequence packed with others can differ
