@@ -479,26 +479,40 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // and 94, 1024 201 and 224, 8192 1550 and 1422.  Segments for more waves than these cost
 // more again (8192 tokens in 6: 154), and so do segments of one 64-token chunk (4096
 // tokens, 4 heads, fp32: 89 us in 16 segments, 99 in 32).
-int segment_len(int64_t T, int Hv, int Dv, bool tc, bool backward) {
-  const int ch = tc ? 128 : 64, ctas = tc ? Hv : Hv * (Dv / DCT), sms = sm_count();
-  const double scans = backward ? 3 : 1, states = backward ? 2 : 1;
-  const double chunk = scans * (tc ? 3.2 : 11.8), cut = chunk + states * (tc ? 1.2 : 4.3);
-  const double fixed = tc ? (backward ? 28 : 22) : 25;
-  const int64_t n = std::max<int64_t>(1, (T + ch - 1) / ch);
-  int64_t best = n;
-  double least = chunk * (double)n;
-  for (int waves = 1; waves <= (tc ? 1 : 2); ++waves) {
-    const int64_t s = (int64_t)waves * sms / ctas;
-    if (s < 2) continue;
-    const int64_t per = std::max<int64_t>(tc ? 1 : 2, (n + s - 1) / s);
-    const double us = fixed + cut * (double)(per * waves);
-    if (us < least) {
-      least = us;
-      best = per;
-    }
+struct Cutting {
+  int ch, max_waves;           // tokens of a chunk; waves of segments that are tried
+  int64_t min_per, ctas, sms;  // chunks of the shortest segment; CTAs of one over all heads
+  double chunk, cut, fixed;    // a chunk uncut and cut, and what cutting costs (us)
+  Cutting(int Hv, int Dv, bool tc, bool backward)
+      : ch(tc ? 128 : 64), max_waves(tc ? 1 : 2), min_per(tc ? 1 : 2), ctas(tc ? Hv : Hv * (Dv / DCT)),
+        sms(sm_count()) {
+    chunk = (backward ? 3 : 1) * (tc ? 3.2 : 11.8);
+    cut = chunk + (backward ? 2 : 1) * (tc ? 1.2 : 4.3);
+    fixed = tc ? (backward ? 28 : 22) : 25;
   }
-  return (int)(best * ch);
-}
+  int64_t chunks(int64_t T) const { return std::max<int64_t>(1, (T + ch - 1) / ch); }
+  int segment_len(int64_t T) const {
+    const int64_t n = chunks(T);
+    int64_t best = n;
+    double least = chunk * (double)n;
+    for (int waves = 1; waves <= max_waves; ++waves) {
+      const int64_t s = waves * sms / ctas;
+      if (s < 2) continue;
+      const int64_t per = std::max(min_per, (n + s - 1) / s);
+      const double us = fixed + cut * (double)(per * waves);
+      if (us < least) {
+        least = us;
+        best = per;
+      }
+    }
+    return (int)std::min<int64_t>(best * ch, INT32_MAX);
+  }
+  // At least T' / (its segment length) of every T' <= T that is cut.
+  int64_t most(int64_t T) const {
+    const int64_t n = chunks(T), s = max_waves * sms / ctas;
+    return s < 2 || chunk * (double)n <= fixed + cut * (double)min_per ? 0 : std::min(s, n / min_per);
+  }
+};
 
 struct Layout {
   int L;
@@ -506,13 +520,17 @@ struct Layout {
   size_t units, nat, tr, part, total;
 };
 
-Layout layout(int64_t N, int64_t T, int Hqk, int Hv, int Dk, int Dv, bool tc, bool backward) {
+// Where things lie in a workspace; `reserve`: as for the call of at most N sequences and
+// T tokens that needs most, so that a workspace of its size serves all of them.
+Layout layout(int64_t N, int64_t T, int Hqk, int Hv, int Dk, int Dv, bool tc, bool backward, bool reserve = false) {
   Layout l;
-  l.L = segment_len(T, Hv, Dv, tc, backward);
-  const bool one = T <= l.L;
-  l.max_seg = one ? N : T / l.L + N;
-  l.max_cut = one ? 0 : std::min<int64_t>(N, T / l.L);
-  l.max_cut_seg = one ? 0 : T / l.L + l.max_cut;
+  const Cutting c(Hv, Dv, tc, backward);
+  l.L = c.segment_len(T);
+  const int64_t per_seq = reserve ? c.most(T) : T <= l.L ? 0 : T / l.L;
+  const bool one = per_seq == 0;
+  l.max_seg = per_seq + N;
+  l.max_cut = std::min(N, per_seq);
+  l.max_cut_seg = per_seq + l.max_cut;
   size_t at = kWorkspaceHeaderBytes;
   l.units = at;
   if (!one) at = round_up(at + sizeof(int4) * (size_t)(l.max_seg + l.max_cut_seg + l.max_cut), 1024);
@@ -532,8 +550,8 @@ Layout layout(int64_t N, int64_t T, int Hqk, int Hv, int Dk, int Dv, bool tc, bo
 
 size_t linear_workspace_bytes(int64_t N, int64_t T, int Hqk, int Hv, int Dk, int Dv, bool backward) {
   // of both forms: the output's type, which decides between them, is not known here
-  return std::max(lin::layout(N, T, Hqk, Hv, Dk, Dv, true, backward).total,
-                  lin::layout(N, T, Hqk, Hv, Dk, Dv, false, backward).total);
+  return std::max(lin::layout(N, T, Hqk, Hv, Dk, Dv, true, backward, true).total,
+                  lin::layout(N, T, Hqk, Hv, Dk, Dv, false, backward, true).total);
 }
 
 namespace lin {

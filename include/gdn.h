@@ -432,6 +432,7 @@ int32_t gdn_prefill_backward_sequential(const void *q, const void *k, const void
  * multiprocessor's share the segment tables and one starting state per (segment of a
  * sequence longer than that share, value head); for the backward also the transposed
  * states and, where Hv > Hqk, an fp32 [T, Hv, Dk] buffer of per-value-head dq or dk.
+ * A workspace of this size also serves every call of fewer sequences and tokens.
  */
 size_t gdn_linear_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens,
                                          int32_t num_qk_heads, int32_t num_v_heads,

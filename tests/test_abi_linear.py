@@ -100,6 +100,16 @@ def test_workspace_sizes(lib):
     assert size(1, 8, 2, 5, 64, 64, 0, 0) == 0 and size(1, 8, 2, 6, 64, 64, 7, 0) == 0
 
 
+@pytest.mark.parametrize("Hqk,Hv", [(1, 1), (2, 8), (16, 48), (25, 75), (100, 200)])
+@pytest.mark.parametrize("backward", [0, 1])
+def test_workspace_serves_smaller_calls(lib, Hqk, Hv, backward):
+    last = 0
+    for T in [*range(0, 6000, 64), 18944, 19200, 19300, 40000, 262144, 2 ** 31 - 1]:
+        sizes = [lib.gdn_linear_prefill_workspace_size(N, T, Hqk, Hv, 128, 128, 0, backward) for N in (1, 2, 70, 1000)]
+        assert sizes == sorted(sizes) and sizes[0] >= last
+        last = sizes[0]
+
+
 @pytest.mark.parametrize("call", [decode, tree, commit])
 def test_common_refusals(lib, call):
     assert call(lib, Hv=5) == BAD and call(lib, Hqk=0) == BAD and call(lib, Hv=-6) == BAD

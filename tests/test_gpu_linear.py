@@ -405,3 +405,23 @@ def test_cut_sequences_among_many(dtype):
     for got, w, m, name in zip((dq, dk, dv, ds0), *grads_ref(x, cu, S0, do, dsf, 1.0), ("dq", "dk", "dv", "dS0")):
         exact = dtype == "fp32" or name == "dS0"
         R.check(got, w, m, tol if exact else 2 * R.UB16, name, R.U32 if exact else R.UB16)
+
+
+def test_workspace_of_a_larger_call():
+    """A workspace made for more tokens serves fewer, which are cut more finely."""
+    x, _, _, r = make([19200], 1, 1, 64, 64, "bf16", seed=51)
+    do = r(19200, 1, 64).to(torch.bfloat16).to(DEV)
+    a = dev(x["q"], x["k"], x["v"])
+    g = x["g"].to(DEV)
+    ws = [torch.zeros(api.linear_prefill_workspace_size(1, 19200, 1, 1, 64, 64, torch.bfloat16, b), dtype=torch.uint8,
+                      device=DEV) for b in (False, True)]
+    for T in (19200, 18944, 9000, 300, 1):
+        part = [t[:T] for t in a]
+        for odt in (torch.bfloat16, torch.float32):
+            got = api.linear_prefill(*part, g, o_dtype=odt, workspace=ws[0])
+            want = api.linear_prefill(*part, g, o_dtype=odt)
+            assert all(torch.equal(u, v) for u, v in zip(got, want))
+        got = api.linear_prefill_backward(*part, g, do[:T], workspace=ws[1])
+        want = api.linear_prefill_backward(*part, g, do[:T])
+        assert all(torch.equal(u, v) for u, v in zip(got, want) if u is not None)
+    assert all(api.get_device_status(w) == api.GDN_OK for w in ws)
