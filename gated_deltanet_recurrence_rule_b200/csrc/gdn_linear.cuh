@@ -32,11 +32,12 @@ namespace lin {
 struct Scan {
   const void *a, *b, *c;  // [T, Ha | Hb | Hc, Da | Da | Dc], element type T
   int Ha, Hb, Hc;         // their heads: Hv or Hqk
-  void *out;              // [T, Hv, Dc], NULL: states only
+  void *out;              // [T, Hv, Dc], and NULL where T = 0
   const float *g;         // [Hv]
   const int32_t *cu;
   int N, T, Hv, Da, Dc;
   int back;
+  int states_only;        // what each segment adds, into seg_state; no outputs
   float s_intra, s_inter, s_upd;
   const int4 *units;         // [segments] the segments, longest first (below); NULL where each
                              // sequence is one segment

@@ -427,7 +427,7 @@ static cudaError_t launch_scan_t(const Scan &p, int units, cudaStream_t stream) 
   static_assert(bytes <= 232448, "shared memory of a CTA");
   const unsigned grid = (unsigned)units * (unsigned)(p.Dc / DCT);
   cudaError_t e;
-  if (p.out) {
+  if (!p.states_only) {
     if ((e = set_smem_once(scan_kernel<T, TO, DA, true>, bytes, f1)) != cudaSuccess) return e;
     return launch_pdl(scan_kernel<T, TO, DA, true>, dim3(grid), dim3(NTHREADS), bytes, stream, p);
   }
@@ -576,9 +576,10 @@ static cudaError_t run_plan(const Scan &p, const Layout &l, unsigned char *ws, P
   return launch_pdl(plan_segments_kernel, dim3(1), dim3(1024), 0, stream, p.cu, p.N, p.T, l.L, plan, p.status);
 }
 
-// What the segments add to the states, into p.seg_state (p.out is NULL).
+// What the segments add to the states, into p.seg_state.
 static cudaError_t run_states(Scan p, bool tc, const Plan &plan, int dtype, cudaStream_t stream) {
   p.units = plan.cut_units;
+  p.states_only = 1;
   return run_scan(p, tc, plan.max_cut_seg * p.Hv, dtype, dtype, stream);
 }
 

@@ -916,7 +916,7 @@ cudaError_t launch_scan_tc(const Scan &p, int units, int out_dtype, cudaStream_t
   CUtensorMap ma, mb, mc, mo;
   if (!make_map(&mb, p.b, p.Hb, p.T, p.Da) || !make_map(&mc, p.c, p.Hc, p.T, p.Dc)) return cudaErrorInvalidValue;
   cudaError_t e;
-  if (!p.out) {
+  if (p.states_only) {
     if ((e = set_smem_once(scan_state_tc_kernel, SMEM_STATE, f0)) != cudaSuccess) return e;
     return launch_pdl(scan_state_tc_kernel, dim3((unsigned)units), dim3(NTHREADS), SMEM_STATE, stream, mb, mc, p);
   }
