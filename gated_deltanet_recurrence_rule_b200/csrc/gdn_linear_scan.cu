@@ -653,7 +653,7 @@ cudaError_t launch_linear_backward(const void *q, const void *k, const void *v, 
   auto into = [&](Scan p, void *out) -> cudaError_t {
     p.out = grouped ? part : out;
     cudaError_t r = run_scan(p, tc, units, dtype, grouped ? GDN_DTYPE_FP32 : dtype, stream);
-    if (r != cudaSuccess || !grouped) return r;
+    if (r != cudaSuccess || !grouped || T == 0) return r;  // (no rows: a grid of no blocks is refused)
     const size_t quads = (size_t)T * Hqk * Dk / 4;
     const unsigned blocks = (unsigned)((quads + 255) / 256);
     const float *from = part;

@@ -59,3 +59,9 @@ def backward_of_empty(N, Hqk, Hv, dtype):
 @pytest.mark.parametrize("N", [1, 3])
 def test_backward_of_empty_sequences(N, dtype):
     backward_of_empty(N, 3, 3, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("N", [1, 3])
+def test_backward_of_empty_sequences_with_shared_heads(N, dtype):
+    backward_of_empty(N, 2, 6, dtype)
