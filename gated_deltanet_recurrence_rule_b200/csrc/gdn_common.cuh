@@ -83,6 +83,11 @@ __device__ __forceinline__ float beta_raw(float b) { return 1.f / (1.f + expf(-b
 // 1 / |x| from the sum of squares, 0 for a zero row (which then stays zero).
 __device__ __forceinline__ float inv_norm(float ss) { return ss > 0.f ? 1.f / sqrtf(ss) : 0.f; }
 
+// The log of a head's decay lam.  A decay below e^-30 ~ 1e-13 is taken as e^-30, below
+// the resolution of an fp32 sum, so that its powers are defined at lam = 0 too (0 * -inf
+// is not).  A NaN stays one (fmaxf would return the floor and hide it).
+__device__ __forceinline__ float floor_decay(float g) { return g < -30.f ? -30.f : g; }
+
 // Streaming (evict-first) 128-bit global load / store for data touched once.
 __device__ __forceinline__ float4 ld_stream(const float4 *p) { return __ldcs(p); }
 __device__ __forceinline__ void st_stream(float4 *p, float4 v) { __stcs(p, v); }

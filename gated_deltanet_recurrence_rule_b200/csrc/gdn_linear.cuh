@@ -90,8 +90,7 @@ __device__ __forceinline__ bool get_unit(const Scan &p, int u, Unit &w) {
   return true;
 }
 
-// A decay below e^-30 is taken as e^-30 (gdn_rows.cuh says why).
-__device__ __forceinline__ float head_decay(const Scan &p, int h) { return fmaxf(p.g[h], -30.f); }
+__device__ __forceinline__ float head_decay(const Scan &p, int h) { return floor_decay(p.g[h]); }
 
 // Element (i, j) of a sequence's initial state.
 __device__ __forceinline__ float initial_state(const Scan &p, const Unit &w, int i, int j) {

@@ -66,7 +66,7 @@ linear_decode_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *
 #pragma unroll
   for (int x = 0; x < BATCH; ++x) L::load(raw[x], Sin + (size_t)(x * 4 + rr) * DK, c8);
 
-  const float gh = fmaxf(g[h], rows::kDecayFloor);
+  const float gh = floor_decay(g[h]);
 #pragma unroll 2
   for (int x = tid; x < Tn * (DK / 8); x += 128) {
     const int t = x / (DK / 8), d = 8 * (x - t * (DK / 8));

@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(256) prefix_kernel(const Prefix p) {
   const int ci = unit / p.Hv, h = unit - ci * p.Hv;
   const int4 seq = p.cuts[ci];
   const int n = seq.x, s0 = seq.y, cnt = seq.z, len = seq.w;
-  const float gh = fmaxf(p.g[h], -30.f);
+  const float gh = floor_decay(p.g[h]);
   if (n < 0) return;
   const int i0 = 32 * (tl / (p.Da / 32)), j0 = 32 * (tl % (p.Da / 32));
   const int r = threadIdx.x >> 3, c = 4 * (threadIdx.x & 7);

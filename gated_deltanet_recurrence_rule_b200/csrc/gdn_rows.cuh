@@ -16,10 +16,6 @@
 namespace gdn {
 namespace rows {
 
-// A decay below e^-30 ~ 1e-13 is taken as e^-30, below the resolution of an
-// fp32 sum, so that its powers are defined at lam = 0 too (0 * -inf is not).
-constexpr float kDecayFloor = -30.f;
-
 // Four rows' sums over the 8 lanes of a row group, each lane c8 left with the sum of
 // row c8 mod 4 (two rows change places at each of two steps: 4 shuffles, not 12).
 __device__ __forceinline__ float reduce4(const float p[4], int c8) {

@@ -184,7 +184,7 @@ decode_tree_kernel(const Params p) {
     const float gv = i < M ? p.g[delta ? gi : (size_t)h] : 0.f, bv = i < M && delta ? p.beta[gi] : 1.f;
     par[i] = pi;
     bad |= pi >= i;
-    alpha[i] = delta ? (p.raw ? alpha_raw(gv) : expf(gv)) : expf(fmaxf(gv, rows::kDecayFloor));
+    alpha[i] = delta ? (p.raw ? alpha_raw(gv) : expf(gv)) : expf(floor_decay(gv));
     bet[i] = p.raw ? beta_raw(bv) : bv;
   }
   if (XP > 1) {  // fp32: as XP bf16 terms, four loads of a thread in flight
@@ -510,7 +510,7 @@ tree_commit_kernel(const CommitParams p) {
       al[t] = p.raw ? alpha_raw(p.g[gi]) : expf(p.g[gi]);
       bt[t] = p.raw ? beta_raw(p.beta[gi]) : p.beta[gi];
     } else {
-      al[t] = expf(fmaxf(p.g[h], rows::kDecayFloor));
+      al[t] = expf(floor_decay(p.g[h]));
       bt[t] = 1.f;
     }
   }

@@ -423,7 +423,8 @@ int32_t gdn_prefill_backward_sequential(const void *q, const void *k, const void
  *
  * Heads, packed sequences, state layout, slot pools and element types are those
  * of the entry points above.  g is [Hv] fp32, <= 0; values below -30 (and -inf,
- * lam = 0) are taken as -30: e^-30 is below the resolution of an fp32 sum.  (The
+ * lam = 0) are taken as -30: e^-30 is below the resolution of an fp32 sum.  A NaN
+ * makes every result of its head that a token has reached NaN, and no other.  (The
  * pages describe the gated rule only; this is its relative without the erase.)
  *
  * gdn_linear_prefill_workspace_size: bytes of device workspace that

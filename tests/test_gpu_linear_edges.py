@@ -65,3 +65,67 @@ def test_backward_of_empty_sequences(N, dtype):
 @pytest.mark.parametrize("N", [1, 3])
 def test_backward_of_empty_sequences_with_shared_heads(N, dtype):
     backward_of_empty(N, 2, 6, dtype)
+
+
+LENS = {"whole": [150, 0, 70], "cut": [2300, 0, 70]}  # (cut: in segments, in both forms)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens", sorted(LENS))
+def test_a_decay_that_is_no_number(dtype, lens):
+    """A NaN in g makes everything of its head NaN that a token has reached, and
+    nothing else: the other heads' bits are those without it."""
+    L, Hqk, Hv, bad = LENS[lens], 2, 4, 1
+    x, cu, S0, r = make(L, Hqk, Hv, 128, 64, dtype, seed=71)
+    do, dsf = r(sum(L), Hv, 64).to(DT[dtype]), r(len(L), Hv, 64, 128)
+    cut = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    q, k, v, g, do, s0, dsf = dev(x["q"], x["k"], x["v"], x["g"], do, S0, dsf)
+    gn = g.clone()
+    gn[bad] = float("nan")
+
+    def calls(g):
+        o, f = api.linear_prefill(q, k, v, g, cu_seqlens=cut, initial_state=s0, o_dtype=DT[dtype])
+        return o, f, *api.linear_prefill_backward(q, k, v, g, do, cu_seqlens=cut, initial_state=s0, d_final_state=dsf)
+
+    want, got = calls(g), calls(gn)
+    torch.cuda.synchronize()
+    heads = lambda n: [h for h in range(n) if h != (bad if n == Hv else bad // (Hv // Hqk))]  # noqa: E731
+    for name, a, b in zip(("o", "final_state", "dq", "dk", "dv", "d_initial_state"), want, got):
+        assert torch.isfinite(a).all()
+        rest = heads(a.shape[1])
+        mine = [h for h in range(a.shape[1]) if h not in rest]
+        assert torch.equal(a[:, rest], b[:, rest]), name
+        if "state" in name:
+            assert torch.isnan(b[[0, 2]][:, mine]).all() and torch.equal(a[1], b[1]), name  # (1 is empty)
+        else:
+            assert torch.isnan(b[:, mine]).all(), name
+
+
+@pytest.mark.parametrize("Tn", [1, 5])
+def test_a_decay_that_is_no_number_in_decode_and_trees(Tn):
+    """The same for the tokens of a decode call, the nodes of a tree and its commit;
+    where no node is accepted, the state is copied whatever its decay."""
+    B, Hv, bad = 3, 4, 2
+    gen = torch.Generator().manual_seed(73)
+    r = lambda *s: torch.randn(*s, generator=gen).to(DEV)  # noqa: E731
+    q, k, v, g = r(B, Tn, 2, 64), r(B, Tn, 2, 64), r(B, Tn, Hv, 128), -torch.rand(Hv, generator=gen).to(DEV)
+    pool = r(B, Hv, 128, 64)
+    parent = torch.tensor([[i // 2 - (i == 0) for i in range(Tn)]] * B, dtype=torch.int32, device=DEV)
+    accept = torch.tensor([Tn - 1, -1, 0], dtype=torch.int32, device=DEV)
+    gn = g.clone()
+    gn[bad] = float("nan")
+
+    def calls(g):
+        decoded, committed = torch.zeros_like(pool), torch.zeros_like(pool)
+        o = api.linear_decode_tokens(q, k, v, g, pool, decoded)
+        t = api.decode_tree(q, k, v, g, None, parent, pool)
+        api.tree_commit(k, v, g, None, parent, accept, pool, committed)
+        return o.movedim(2, 0), t.movedim(2, 0), decoded.movedim(1, 0), committed.movedim(1, 0)
+
+    want, got = calls(g), calls(gn)
+    torch.cuda.synchronize()
+    rest = [h for h in range(Hv) if h != bad]
+    for name, a, b in zip(("decode o", "tree o", "decoded state", "committed state"), want, got):
+        assert torch.isfinite(a).all() and torch.equal(a[rest], b[rest]), name
+        assert torch.isnan(b[bad][[0, 2]]).all(), name
+        assert torch.equal(b[bad][1], pool[1, bad]) if name == "committed state" else torch.isnan(b[bad][1]).all(), name
