@@ -522,6 +522,8 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         for (int i = 0; i < 64; i += 4) load4(reinterpret_cast<const float *>(at) + i, X + i);
       }
     }
+    // (what this thread wrote there by ordinary stores comes before the tiles that TMA writes there)
+    if (!by_copy) fence_proxy_async_smem();
     arrive(B_X0 + 1);
     auto put_x = [&]() {
       unsigned char *xo = smem + OFF_X + hf * 16384;

@@ -93,3 +93,35 @@ def check(x, ref, mag, rel, what, stored=0.0):
     bad = ~(err <= bound)
     assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} beyond the bound, worst ratio "
                            f"{float((err / bound).nan_to_num(float('inf')).max()):.3g}")
+
+
+def scan_grads(q, k, v, g, cu, S0, do, dsf, scale=1.0):
+    """Gradients of ``scan``'s o and final states, given theirs: ((dq, dk, dv, dS0),
+    the magnitudes of the same), token by token from the formulas."""
+    q, k, v, g, do, S0, dsf = (d64(x) for x in (q, k, v, g, do, S0, dsf))
+    T, Hv, Dv = v.shape
+    N, Hqk, Dk = len(cu) - 1, *k.shape[1:]
+    rep = torch.arange(Hv) // (Hv // Hqk)
+    zero = torch.zeros(N, Hv, Dv, Dk, dtype=torch.float64)
+    S0, dsf = zero if S0 is None else S0, zero if dsf is None else dsf
+    lam = g.clamp_min(-30.0).exp()[:, None, None]
+    out = []
+    for q, k, v, do, S0, dsf, s in ((q, k, v, do, S0, dsf, scale),
+                                    (q.abs(), k.abs(), v.abs(), do.abs(), S0.abs(), dsf.abs(), abs(scale))):
+        q, k = q[:, rep], k[:, rep]
+        dq, dk, dv = torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
+        dS0 = dsf.clone()
+        for n in range(N):
+            S, D = S0[n], dsf[n]
+            for t in range(cu[n], cu[n + 1]):
+                S = lam * S + v[t, :, :, None] * k[t, :, None, :]
+                dq[t] = s * torch.einsum("hvd,hv->hd", S, do[t])
+            for t in range(cu[n + 1] - 1, cu[n] - 1, -1):
+                D = D + s * do[t, :, :, None] * q[t, :, None, :]
+                dk[t] = torch.einsum("hvd,hv->hd", D, v[t])
+                dv[t] = torch.einsum("hvd,hd->hv", D, k[t])
+                D = lam * D
+            dS0[n] = D
+        dq, dk = (x.unflatten(1, (Hqk, Hv // Hqk)).sum(2) for x in (dq, dk))
+        out.append((dq, dk, dv, dS0))
+    return out

@@ -129,3 +129,25 @@ def test_a_decay_that_is_no_number_in_decode_and_trees(Tn):
         assert torch.isfinite(a).all() and torch.equal(a[rest], b[rest]), name
         assert torch.isnan(b[bad][[0, 2]]).all(), name
         assert torch.equal(b[bad][1], pool[1, bad]) if name == "committed state" else torch.isnan(b[bad][1]).all(), name
+
+
+def test_backward_from_transposed_states_repeats():
+    """One segment of several chunks a sequence, on every multiprocessor: the starting
+    states of dq and dk are transposed through the place of a later chunk's tiles.  The
+    same bits each time, whatever ran between, and the formula's values."""
+    L, Hv = [300] * 8, 24
+    x, cu, S0, r = make(L, 8, Hv, 128, 128, "bf16", seed=81)
+    do, dsf = r(sum(L), Hv, 128).to(torch.bfloat16), r(len(L), Hv, 128, 128)
+    cut = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    a = dev(x["q"], x["k"], x["v"], x["g"], do)
+    s0, d = dev(S0, dsf)
+    call = lambda s0, d: api.linear_prefill_backward(*a, cu_seqlens=cut, initial_state=s0, d_final_state=d)  # noqa: E731
+    want = call(s0, d)
+    for _ in range(20):
+        call(-3.0 * s0, None)
+        got = call(s0, d)
+        for name, u, w in zip(("dq", "dk", "dv", "d_initial_state"), want, got):
+            assert torch.equal(u, w), name
+    refs, mags = R.scan_grads(x["q"][:300], x["k"][:300], x["v"][:300], x["g"], [0, 300], S0[:1], do[:300], dsf[:1])
+    for name, u, ref, mag in zip(("dq", "dk", "dv"), want, refs, mags):
+        R.check(u[:300], ref, mag, 2 * R.UB16, name, R.UB16)
