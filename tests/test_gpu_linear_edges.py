@@ -151,3 +151,41 @@ def test_backward_from_transposed_states_repeats():
     refs, mags = R.scan_grads(x["q"][:300], x["k"][:300], x["v"][:300], x["g"], [0, 300], S0[:1], do[:300], dsf[:1])
     for name, u, ref, mag in zip(("dq", "dk", "dv"), want, refs, mags):
         R.check(u[:300], ref, mag, 2 * R.UB16, name, R.UB16)
+
+
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (128, 64)])
+def test_gradients_against_aligned_differences(Dk, Dv):
+    """Central differences of the kernels' own forward (fp32) along the sign of each
+    gradient, so that nothing cancels in the derivative: the loss is linear in q, k, v
+    and the initial state one at a time, so a step of any length gives it up to rounding.
+    That is rel32 of every element's magnitude, weighted by the element's gradient; it
+    stays below a hundredth of the derivative, so a gradient that is zero, scaled by
+    1.02 or of the wrong sign is found."""
+    L, Hqk, Hv = [70, 3, 131], 2, 4
+    x, cu, S0, r = make(L, Hqk, Hv, Dk, Dv, "fp32", seed=77)
+    do, dsf = r(sum(L), Hv, Dv), r(len(L), Hv, Dv, Dk)
+    cut = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    vals = [x["q"], x["k"], x["v"], S0]
+    grads = api.linear_prefill_backward(*dev(*vals[:3], x["g"], do), cu_seqlens=cut, initial_state=S0.to(DEV),
+                                        d_final_state=dsf.to(DEV), scale=0.5)
+    refs, _ = R.scan_grads(*vals[:3], x["g"], cu, S0, do, dsf, 0.5)
+
+    def loss(q, k, v, s0):
+        """The loss of the kernels' forward, and how far its roundings may move it."""
+        o, f = api.linear_prefill(*dev(q, k, v, x["g"]), cu_seqlens=cut, initial_state=s0.to(DEV), scale=0.5)
+        ref, om, F, Fm = R.scan(q, k, v, x["g"], cu, s0, 0.5)
+        tol = rel32(L, Dk)
+        off = (R.d64(do).abs() * (tol * om + R.U32 * ref.abs())).sum() + (R.d64(dsf).abs() * (tol * Fm + R.U32 * F.abs())).sum()
+        return float((R.d64(o) * R.d64(do)).sum() + (R.d64(f) * R.d64(dsf)).sum()), float(off)
+
+    for i, (name, grad, ref) in enumerate(zip(("q", "k", "v", "initial state"), grads, refs)):
+        # a step exact in fp32, and sums with it that round once
+        d = (0.25 * ref.sign()).float()
+        ends = [[t + s * d if j == i else t for j, t in enumerate(vals)] for s in (1.0, -1.0)]
+        (a, ea), (b, eb) = (loss(*e) for e in ends)
+        d = (R.d64(ends[0][i]) - R.d64(ends[1][i])) / 2  # the step as it was taken
+        want, allowed = float((ref * d).sum()), (ea + eb) / 2
+        assert allowed <= 0.01 * want, (name, allowed, want)
+        assert abs((a - b) / 2 - want) <= allowed, (name, (a - b) / 2, want, allowed)
+        got = float((R.d64(grad) * d).sum())
+        assert abs((a - b) / 2 - got) <= 2 * allowed, (name, (a - b) / 2, got, allowed)
