@@ -189,3 +189,27 @@ def test_gradients_against_aligned_differences(Dk, Dv):
         assert abs((a - b) / 2 - want) <= allowed, (name, (a - b) / 2, want, allowed)
         got = float((R.d64(grad) * d).sum())
         assert abs((a - b) / 2 - got) <= 2 * allowed, (name, (a - b) / 2, got, allowed)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens", sorted(LENS))
+def test_states_that_are_not_wanted(dtype, lens):
+    """Without a final state, and without the gradient of the initial one, the rest is
+    the definition's (bf16: w C enters in two terms then, so o and dv may differ in
+    rounding from those of a call that returns the state)."""
+    L = LENS[lens]
+    x, cu, S0, r = make(L, 2, 4, 128, 64, dtype, seed=91)
+    do, dsf = r(sum(L), 4, 64).to(DT[dtype]), r(len(L), 4, 64, 128)
+    cut = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    a, (do_, s0, d) = dev(x["q"], x["k"], x["v"], x["g"]), dev(do, S0, dsf)
+    o, f = api.linear_prefill(*a, cu_seqlens=cut, initial_state=s0, output_final_state=False, o_dtype=DT[dtype])
+    *grads, ds0 = api.linear_prefill_backward(*a, do_, cu_seqlens=cut, initial_state=s0, d_final_state=d,
+                                              want_d_initial_state=False)
+    torch.cuda.synchronize()
+    assert f is None and ds0 is None
+    tol, stored = (2 * R.UB16, R.UB16) if dtype == "bf16" else (rel32(L, 128) + 2 * R.U32, R.U32)
+    ref, om, _, _ = R.scan(x["q"], x["k"], x["v"], x["g"], cu, S0)
+    R.check(o, ref, om, tol, "o", stored)
+    refs, mags = R.scan_grads(x["q"], x["k"], x["v"], x["g"], cu, S0, do, dsf)
+    for name, got, ref, mag in zip(("dq", "dk", "dv"), grads, refs, mags):
+        R.check(got, ref, mag, tol, name, stored)
