@@ -507,6 +507,7 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
 #pragma unroll 4
         for (int i = 0; i < 64; ++i)
           *reinterpret_cast<float *>(smem + STAGE + slot + 4 * i) = initial_state(p, u, row, 64 * hf + i);
+        fence_proxy_async_smem();  // these ordinary stores come before the tiles that TMA writes there
       }
       arrive(B_X0);
     }
@@ -522,8 +523,6 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         for (int i = 0; i < 64; i += 4) load4(reinterpret_cast<const float *>(at) + i, X + i);
       }
     }
-    // (what this thread wrote there by ordinary stores comes before the tiles that TMA writes there)
-    if (!by_copy) fence_proxy_async_smem();
     arrive(B_X0 + 1);
     auto put_x = [&]() {
       unsigned char *xo = smem + OFF_X + hf * 16384;
