@@ -473,7 +473,9 @@ def linear_prefill(q, k, v, g, cu_seqlens=None, initial_state=None, output_final
     g [Hv] fp32 (log of the head's decay, <= 0); everything else as in
     ``prefill``.  ``workspace``: a zero-filled uint8 CUDA tensor of
     ``linear_prefill_workspace_size`` bytes, reused across calls, or None.
-    bf16 inputs with ``o_dtype`` bf16 run on tcgen05; anything else at fp32 accuracy.
+    bf16 inputs with ``o_dtype`` bf16 run on tcgen05; anything else, the default
+    fp32 ``o`` included, at about fp32 accuracy in several times the time (8192
+    tokens at 16/48 heads of 128: 0.99 ms against 0.14).
     Returns (o [T, Hv, Dv], final_state or None)."""
     lib = load()
     dev, T, N, Hqk, Hv, Dk, Dv, cu_seqlens = _check_packed(q, k, v, g, cu_seqlens, "linear_prefill")

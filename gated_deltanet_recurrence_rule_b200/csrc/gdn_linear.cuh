@@ -110,9 +110,9 @@ __device__ __forceinline__ float start_state(const Scan &p, const Unit &w, int i
 // ---- host ----
 // The CUDA-core-and-mma.sync form, every type and head dim (gdn_linear_scan.cu).
 cudaError_t launch_scan(const Scan &p, int units, int dtype, int out_dtype, cudaStream_t stream);
-// The tcgen05 form (gdn_linear_tc.cu): bf16 operands.  Its states
-// are exact to fp32; its outputs carry the roundings of bf16 operands, whatever type
-// they are stored in.
+// The tcgen05 form (gdn_linear_tc.cu): bf16 operands.  States that are returned or
+// handed to another segment are summed from products of all 24 bits; its outputs carry
+// the roundings of bf16 operands, whatever type they are stored in.
 bool scan_tc_supported(const Scan &p, int dtype);
 cudaError_t launch_scan_tc(const Scan &p, int units, int out_dtype, cudaStream_t stream);
 

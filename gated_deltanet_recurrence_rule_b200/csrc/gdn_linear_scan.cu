@@ -478,7 +478,8 @@ size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // and 130; its backward, 1024 tokens 135 and 118.  The other form (fp32), 256 tokens 59
 // and 94, 1024 201 and 224, 8192 1550 and 1422.  Segments for more waves than these cost
 // more again (8192 tokens in 6: 154), and so do segments of one 64-token chunk (4096
-// tokens, 4 heads, fp32: 89 us in 16 segments, 99 in 32).
+// tokens, 4 heads, fp32: 89 us in 16 segments, 99 in 32).  Other head counts and head dim 64 go by the
+// same costs, which were not timed for them.
 struct Cutting {
   int ch, max_waves;           // tokens of a chunk; waves of segments that are tried
   int64_t min_per, ctas, sms;  // chunks of the shortest segment; CTAs of one over all heads

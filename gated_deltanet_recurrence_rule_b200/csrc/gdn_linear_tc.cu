@@ -20,13 +20,17 @@
 //
 // Bound and measured (8192 tokens, 16/48 heads of 128).  The outputs kernel takes 76 us
 // at 243 MB of HBM traffic, 3.0 TB/s, with the tensor pipe active 39 % of the time: the
-// products read two 32 KB operands from shared memory each, which every chunk's loads,
-// X, P and output tiles pass through as well, about 5,600 cycles a chunk of that against
-// 3,700 for the chunk's share of HBM.  The states kernel takes 40 us.  The whole prefill
-// takes 130 us by itself and 140 in a loop of many, where the board is at its power limit
-// (980 W) and the clock falls to 1.67 GHz; a packed batch of 65,000 tokens 664 and 770 (1.53
-// GHz).  A batch of 256 prompts of 100 tokens takes 897 us: one CTA per (prompt, head),
-// 10.8 us each, whose start and end do not overlap with another's.
+// products read 224 KB of operands a chunk from shared memory (A, B, X, C, and B again
+// for the second term of w C), and loads, w C, X and the output tiles move as much again:
+// about 450 KB or 3,500 cycles of the 5,800 that a chunk takes, beside 3,000 for its share
+// of HBM.  So none of the three is full (shared memory 44 %), and the rest is waiting:
+// there is one P in tensor memory, and the next chunk's is issued after the product with
+// this one's, which waits for the warps that form P and scale A X^T.  The states kernel
+// takes 40 us.  The whole prefill takes 130 us by itself and 140 in a loop of many, where
+// the board is at its power limit (980 W) and the clock falls to 1.67 GHz; a packed batch
+// of 65,000 tokens 664 and 770 (1.53 GHz).  A batch of 256 prompts of 100 tokens takes 897
+// us: one CTA per (prompt, head), 10.8 us each, whose start and end do not overlap with
+// another's.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -447,12 +447,18 @@ size_t gdn_linear_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens,
  * 256-byte aligned, zero-filled once; its first word is the sticky status word
  * (gdn_get_device_status), its second the limit of bounded waits, as there.
  *
- * bf16 inputs with bf16 o run on the tensor cores (tcgen05), with
- * the state in fp32 and its increments from products exact to fp32; the state and
- * the token x token products are rounded to bf16 once, as operands of o, which is
- * itself rounded to bf16.  Everything else runs on warp-level tf32 MMAs with split
- * operands, at about fp32 accuracy.  Rows past a sequence's end are neither read
- * into its results nor written.
+ * bf16 inputs with bf16 o run on the tensor cores (tcgen05), with the state and its
+ * sums in fp32.  The decayed v enters the state's increments in bf16 terms: three (all
+ * 24 bits) where the state is returned or handed to a later part of its sequence, two
+ * (16 bits) where it only serves outputs.  The state and the token x token products are
+ * rounded to bf16 once, as operands of o, which is itself rounded to bf16.  Everything
+ * else, fp32 o from bf16 inputs included, runs on warp-level tf32 MMAs with split
+ * operands, at about fp32 accuracy and several times the time.  Rows past a sequence's
+ * end are neither read into its results nor written.
+ *
+ * total_tokens = 0 copies initial_state (zeros where NULL) to final_state.  Where
+ * cu_seqlens is inconsistent (GDN_ERR_BAD_SEQLENS in the status word), the results of
+ * the call are undefined; nothing is read or written out of bounds.
  *
  * A token that is not finite may reach the outputs of its whole chunk (128 tokens of its sequence on the tensor
  * cores, 64 otherwise), earlier ones included, as well as all later ones; never those
@@ -475,11 +481,14 @@ int32_t gdn_linear_prefill(const void *q, const void *k, const void *v, const fl
  *     dq_t = scale S_t^T d_o_t,  dk_t = D_t^T v_t,  dv_t = D_t k_t,
  *     d_initial_state = lam D_1,
  * three scans of the forward's kind.  Training keeps the inputs' precision: d_o,
- * dq, dk and dv have q's element type (dtype), the states are fp32.
+ * dq, dk and dv have q's element type (dtype), the states are fp32.  bf16 gradients
+ * carry the same two roundings of operands as a bf16 o.
  *
  *   d_o [T, Hv, Dv], dq, dk [T, Hqk, Dk], dv [T, Hv, Dv]   dtype
  *   initial_state, d_final_state   [num_seqs, Hv, Dv, Dk] fp32, or NULL for zeros
  *   d_initial_state                the same shape, or NULL to skip
+ * No output may overlap an input.  total_tokens = 0 copies d_final_state (zeros where
+ * NULL) to d_initial_state.
  * dq and dk of a query/key head sum over its value heads in a fixed order in fp32
  * (results do not depend on scheduling).  The call is stream-ordered and can be
  * captured in a CUDA graph.
@@ -553,7 +562,8 @@ int32_t gdn_decode_tree(const void *q, const void *k, const void *v, const float
  * The state after the accepted node of each tree, from the same k, v, g, beta and
  * parent as gdn_decode_tree was given: state_out[dst_slot[b]] becomes the state
  * after node accept[b], the cached state itself (a copy) where accept[b] = -1.
- * fp32 arithmetic along the path; a bf16 state is rounded once.
+ * fp32 arithmetic along the path; a bf16 state is rounded once.  batch = 0 or
+ * nodes = 0 is a valid no-op: nothing is written.
  *
  *   accept      [batch] int32, device: a node of tree b, or -1
  *   state_in, state_out, src_slot, dst_slot, num_slots   as for gdn_decode_tokens
