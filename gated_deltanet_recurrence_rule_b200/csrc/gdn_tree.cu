@@ -53,6 +53,33 @@ __device__ __forceinline__ void split4(const float x[4], uint32_t (*w)[2]) {
   }
 }
 
+// d += A B with A in PA and B in PB terms, products whose weight is below the last term
+// kept left out.  A tensor core cuts what an addition shifts out of 24 bits, always
+// towards zero: with three terms in B (fp32 inputs), a K step is summed apart, small
+// products first, and added once, rounded to nearest.  (With all of them added to d
+// as they come, 48 cuts in a row at the size of d, fp32 trees were off by 9.6e-7 in rms where
+// they are by 1e-7 now; 64 trees of 32 nodes took 228 us against 237, of 16 nodes 93 against
+// 102.  Three terms against one, 24 cuts, are off by 4e-7 and stay as they are.)
+template <int PA, int PB>
+__device__ __forceinline__ void mma_terms(float *d, const uint32_t (*a)[4], const uint32_t (*b)[2]) {
+  constexpr int P = PA > PB ? PA : PB;
+  if (PB < 3) {
+#pragma unroll
+    for (int tb = 0; tb < PB; ++tb)
+#pragma unroll
+      for (int ta = 0; ta < PA && ta + tb < P; ++ta) mma_16x8x16(d, a[ta], b[tb]);
+    return;
+  }
+  float s[4] = {};
+#pragma unroll
+  for (int w = P - 1; w >= 0; --w)
+#pragma unroll
+    for (int tb = 0; tb < PB; ++tb)
+      if (w - tb >= 0 && w - tb < PA) mma_16x8x16(s, a[w - tb], b[tb]);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) d[e] += s[e];
+}
+
 struct Params {
   const void *q, *k, *v;
   const float *g, *beta;  // beta NULL: linear rule, g one per value head
@@ -81,6 +108,9 @@ struct Layout {
   static constexpr int IDX = AC + MP * MP * 8;                 // [MP][MP] bytes: j
   static constexpr int S = IDX + MP * MP;                      // per-node scalars
   static constexpr int BYTES = S + MP * 4 * 11 + 16;
+  // CTAs of a multiprocessor: 4 or 2 by registers, fewer where shared memory (228 KB, 1 KB
+  // of it for each CTA) does not hold them; the registers then need not be kept for more
+  static constexpr int FIT = 233472 / (BYTES + 1024), MOST = MP <= 32 ? 4 : 2, CTAS = FIT < MOST ? FIT : MOST;
 };
 
 __device__ __forceinline__ void cp_async_16(void *dst, const void *src) {
@@ -105,7 +135,7 @@ __device__ __forceinline__ void cp_async_16(void *dst, const void *src) {
 // pipe 29 %, shared memory 57 % busy, a third of the issue slots used).  8 nodes 54 us,
 // 16 nodes 60; a chain of 32, one node a depth, 180.
 template <typename T, typename ST, int SP, int XP, int DK, int DV, int MP>
-__global__ void __launch_bounds__(DV == 128 && MP == 64 ? 256 : 128, MP <= 32 ? 4 : 2)
+__global__ void __launch_bounds__(DV == 128 && MP == 64 ? 256 : 128, Layout<T, XP, DK, DV, MP>::CTAS)
 decode_tree_kernel(const Params p) {
   pdl_wait();  // nothing is read before the previous kernel on the stream is done
   pdl_allow_next();
@@ -114,7 +144,6 @@ decode_tree_kernel(const Params p) {
   constexpr int NX = 2 * MP / 8;       // 8-node column tiles of [k; q]^T
   constexpr int KS = DK / 16;
   constexpr int PF = MP <= 32 ? 2 : 4; // k steps of S0 in flight (all of it is on its way to L2)
-  constexpr int MAXP = SP > XP ? SP : XP;
   using L = Layout<T, XP, DK, DV, MP>;
   extern __shared__ __align__(16) unsigned char smem[];
   __nv_bfloat16 *X = reinterpret_cast<__nv_bfloat16 *>(smem + L::X);
@@ -292,14 +321,15 @@ decode_tree_kernel(const Params p) {
         a[t][0] = u0.x; a[t][1] = u1.x; a[t][2] = u0.y; a[t][3] = u1.y;
       }
 #pragma unroll
-      for (int n = 0; n < MP / 8; ++n)
+      for (int n = 0; n < MP / 8; ++n) {
+        uint32_t bb[XP][2];
 #pragma unroll
-        for (int tb = 0; tb < XP; ++tb) {
-          const uint2 w = xw(tb, 8 * n + gid, ks);
-          const uint32_t bb[2] = {w.x, w.y};
-#pragma unroll
-          for (int ta = 0; ta + tb < XP; ++ta) mma_16x8x16(acc[n], a[ta], bb);
+        for (int t = 0; t < XP; ++t) {
+          const uint2 w = xw(t, 8 * n + gid, ks);
+          bb[t][0] = w.x; bb[t][1] = w.y;
         }
+        mma_terms<XP, XP>(acc[n], a, bb);
+      }
     }
 #pragma unroll
     for (int n = 0; n < MP / 8; ++n)
@@ -335,15 +365,14 @@ decode_tree_kernel(const Params p) {
 #pragma unroll
     for (int n = 0; n < NX; ++n) {
       if (n < MP / 8 && !delta) continue;  // the linear rule needs no S0 k
+      uint32_t bb[XP][2];
 #pragma unroll
-      for (int tb = 0; tb < XP; ++tb) {
-        const uint2 w = xw(tb, 8 * n + gid, ks);
-        const uint32_t bb[2] = {w.x, w.y};
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int ta = 0; ta < SP && ta + tb < MAXP; ++ta) mma_16x8x16(acc[mt][n], a[mt][ta], bb);
+      for (int t = 0; t < XP; ++t) {
+        const uint2 w = xw(t, 8 * n + gid, ks);
+        bb[t][0] = w.x; bb[t][1] = w.y;
       }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) mma_terms<SP, XP>(acc[mt][n], a[mt], bb);
     }
   }
   __syncthreads();  // X has been used: U and O take its place
