@@ -92,6 +92,28 @@ __device__ __forceinline__ bool get_unit(const Scan &p, int u, Unit &w) {
 
 __device__ __forceinline__ float head_decay(const Scan &p, int h) { return floor_decay(p.g[h]); }
 
+// lam^n for a state that is carried over many stretches of n tokens.  Rounded to fp32 it
+// would be off the same way each time, by as many half steps in the end as there are
+// stretches in the head's memory (2.3e-6 for 17,947 tokens at lam = e^-1e-4).  So a power
+// near one is held as 1 + m, and what a factor's rounding leaves goes into the next one:
+// every product of factors is then right to a step or two.
+struct Power {
+  float value, m;  // value = lam^n, and m = lam^n - 1 where that is above -1/2; else 2
+};
+__device__ __forceinline__ Power decay_power(float g, int n) {
+  const float x = g * (float)n;
+  return Power{expf(x), x > -0.6931f ? expm1f(x) : 2.f};
+}
+struct Carry {
+  float rest;  // 0 at first
+  __device__ __forceinline__ float next(const Power &p) {
+    if (p.m == 2.f) return p.value;
+    const float t = rest + p.m, f = 1.f + t;
+    rest = t - (f - 1.f);
+    return f;
+  }
+};
+
 // Element (i, j) of a sequence's initial state.
 __device__ __forceinline__ float initial_state(const Scan &p, const Unit &w, int i, int j) {
   if (!p.x0) return 0.f;

@@ -141,6 +141,8 @@ __global__ void __launch_bounds__(256) prefix_kernel(const Prefix p) {
   const size_t e0 = ((size_t)n * p.Hv + h) * state + in_state;
   float x[4] = {0.f, 0.f, 0.f, 0.f};
   if (p.x0) load_state4(p.x0, e0, p.x_bf16, x);
+  const Power whole = decay_power(gh, p.L);
+  Carry carry{0.f};
   // what the last segment adds is there only where the final state is wanted
   const int adds = p.xf ? cnt : cnt - 1;
   for (int b = 0; b < cnt; b += 4) {
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(256) prefix_kernel(const Prefix p) {
       }
       if (b + i >= adds) break;
       const int tokens = min(p.L, len - sg * p.L) - (p.back && b + i == 0 ? 1 : 0);
-      const float f = expf(gh * (float)tokens);
+      const float f = carry.next(tokens == p.L ? whole : decay_power(gh, tokens));
 #pragma unroll
       for (int k = 0; k < 4; ++k) x[k] = fmaf(f, x[k], add[i][k]);
     }
@@ -216,6 +218,9 @@ constexpr int DCT = 64;  // columns of out (rows of X) of one CTA
 template <int DA>
 struct Smem {
   float a[C][DA + 4], b[C][DA + 4], c[C][DCT + 8], P[C][C + 4], X[DCT][DA + 4], pw[C + 1];
+  Power whole;  // of a full chunk
+  Carry carry;
+  float lx;     // what the chunk's state is carried over by
 };
 
 // 4 elements on their way from global memory.
@@ -298,6 +303,10 @@ __global__ void __launch_bounds__(NTHREADS) scan_kernel(const Scan p) {
   };
   if (nch > 0) fetch(0);
   if (tid <= C) s.pw[tid] = expf(gh * (float)tid);
+  if (tid == 0) {
+    s.whole = decay_power(gh, C);
+    s.carry.rest = 0.f;
+  }
 
   float X[NX][4];
 #pragma unroll
@@ -321,6 +330,7 @@ __global__ void __launch_bounds__(NTHREADS) scan_kernel(const Scan p) {
     if (OUT) ta.store(&s.a[0][0], DA + 4, tid);
     tb.store(&s.b[0][0], DA + 4, tid);
     tc.store(&s.c[0][0], DCT + 8, tid);
+    if (tid == 0) s.lx = s.carry.next(len - skip == C ? s.whole : decay_power(gh, len - skip));
     __syncthreads();
     if (ci + 1 < nch) fetch(ci + 1);
     if (OUT) {
@@ -397,7 +407,7 @@ __global__ void __launch_bounds__(NTHREADS) scan_kernel(const Scan p) {
         mma_split<false, EX>(dx[n], dxl[n], af, bf);
       }
     }
-    const float lx = s.pw[len - skip];
+    const float lx = s.lx;
 #pragma unroll
     for (int n = 0; n < NX; ++n)
 #pragma unroll

@@ -59,17 +59,24 @@ constexpr uint32_t IDESC_KM = idesc_bf16(128, 128, 0, 1);  // (wC)^T B, P C: B o
 
 struct Weights {        // fp32 tables in shared memory
   float pw[CH + 4];     // lam^i
+  float pm[CH + 4];     // lam^i - 1, or 2 (Power)
+  Carry carry[8];       // of the X warps
   float pwi[CH];        // s_intra lam^i
   float wfull[CH], wtail[CH];  // w_t of a full chunk and of the segment's last one
 };
 
 __device__ __forceinline__ void fill_weights(const Scan &p, Weights *w, float gh, int tail, int tid) {
-  if (tid <= CH) w->pw[tid] = expf(gh * (float)tid);
+  if (tid <= CH) {
+    const Power x = decay_power(gh, tid);
+    w->pw[tid] = x.value;
+    w->pm[tid] = x.m;
+  }
   if (tid < CH) {
     const int rf = p.back ? tid : CH - 1 - tid, rt = p.back ? tid : tail - 1 - tid;
     w->wfull[tid] = p.s_upd * expf(gh * (float)rf);
     w->wtail[tid] = tid < tail ? p.s_upd * expf(gh * (float)rt) : 0.f;
   }
+  if (tid < 8) w->carry[tid].rest = 0.f;
   if (tid < CH) w->pwi[tid] = p.s_intra * expf(gh * (float)tid);
 }
 
@@ -557,7 +564,10 @@ scan_out_tc_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_consta
         arrive(B_VL + hf);
       }
       if (!(ok = warp_wait(B_DX, ph))) break;
-      const float lx = wts->pw[len - skip];
+      Carry carry = wts->carry[warp - 8];
+      const float lx = carry.next(Power{wts->pw[len - skip], wts->pm[len - skip]});
+      __syncwarp();
+      if (lane == 0) wts->carry[warp - 8] = carry;  // (not kept in a register beside X)
 #pragma unroll
       for (int i = 0; i < 64; i += 8) {
         float d[8];
@@ -856,6 +866,7 @@ scan_state_tc_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_cons
       arrive(S_V + (ci & 1));
       return true;
     };
+    Carry carry{0.f};
     bool ok = nch == 0 || terms(0);
     for (int ci = 0; ci < nch && ok; ++ci) {
       if (ci + 1 < nch && !(ok = terms(ci + 1))) break;
@@ -865,7 +876,8 @@ scan_state_tc_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_cons
       tmem_wait_ld();
       tc_fence_before();
       arrive(S_FREE);
-      const float lx = wts->pw[chunk_of(ci) == nch - 1 ? tail : CH];
+      const int len = chunk_of(ci) == nch - 1 ? tail : CH;
+      const float lx = carry.next(Power{wts->pw[len], wts->pm[len]});
 #pragma unroll
       for (int i = 0; i < 32; ++i) X[i] = fmaf(lx, X[i], d[i]);
     }

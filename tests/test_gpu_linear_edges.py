@@ -213,3 +213,27 @@ def test_states_that_are_not_wanted(dtype, lens):
     refs, mags = R.scan_grads(x["q"], x["k"], x["v"], x["g"], cu, S0, do, dsf)
     for name, got, ref, mag in zip(("dq", "dk", "dv"), grads, refs, mags):
         R.check(got, ref, mag, tol, name, stored)
+
+
+@pytest.mark.parametrize("dtype,odtype,chunk", [("bf16", "bf16", 128), ("bf16", "fp32", 64), ("fp32", "fp32", 64)])
+@pytest.mark.parametrize("Hv", [4, 160])
+def test_long_memories(dtype, odtype, chunk, Hv):
+    """Decays whose power over a chunk falls half way between two fp32 numbers, carried
+    over a hundred chunks and more, in segments (4 heads) and in one (160).  Relative rms
+    error of a head's state: a chunk's sum takes at most 24 tensor-core additions, which
+    cut by up to 2^-23 of a sum that grows from nothing, 6 * 2^-23 in the mean; the carry is
+    off by two half steps, 2^-23, at most; additions of chunks round at random.  7 * 2^-23 <
+    2^-20.  (A power rounded to fp32 is off by 2^-25 each time: 2^-18 over 128 chunks.)"""
+    T, D = 16000, 64
+    x, cu, _, _ = make([T], 1, Hv, D, D, dtype, seed=95, init=False)
+    # of many decays those that rounding a chunk's power moves most
+    g = -torch.exp(torch.linspace(-11.5, -9.0, 4001, dtype=torch.float64)).float()
+    p = (g.double() * chunk).exp()
+    g = g[((p.float().double() - p).abs()).argsort(descending=True)[:4]]
+    x["g"][:4] = g
+    o, f = api.linear_prefill(*dev(x["q"], x["k"], x["v"], x["g"]), o_dtype=DT[odtype])
+    torch.cuda.synchronize()
+    ref, _, F, _ = R.scan(x["q"], x["k"], x["v"][:, :4], g, cu)
+    for h in range(4):
+        err = float((R.d64(f[0, h]) - F[0, h]).norm() / F[0, h].norm())
+        assert err <= 2.0 ** -20, f"state of head {h}: {err:.2e}"
