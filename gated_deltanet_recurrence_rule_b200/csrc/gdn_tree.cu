@@ -245,7 +245,9 @@ decode_tree_kernel(const Params p) {
     asm volatile("cp.async.wait_all;" ::: "memory");
     return;
   }
-  // paths: E_ij, E_i0 and the set of strict ancestors of each node
+  // paths: E_ij, E_i0 and the set of strict ancestors of each node.  (Powers of one decay
+  // are taken as such: 64 factors with the same rounding were off by 1.3e-6.)
+  const float gh = delta ? 0.f : floor_decay(p.g[h]);
   for (int i = tid; i < MP; i += NT) {
     unsigned long long m = 0;
     float e = alpha[i];
@@ -254,7 +256,7 @@ decode_tree_kernel(const Params p) {
       m |= 1ull << a;
       AC[i * MP + s] = make_float2(e, e);  // E_ij, times the products below
       idx[i * MP + s] = (unsigned char)a;
-      e *= alpha[a];
+      e = delta ? e * alpha[a] : expf(gh * (float)(s + 2));
     }
     // to a multiple of four: the parent again, with factors of zero
     for (; s & 3; ++s) {
@@ -514,6 +516,9 @@ tree_commit_kernel(const CommitParams p) {
     return;
   }
   const bool delta = p.beta != nullptr;
+  // The linear rule's powers are taken as such (64 factors with the same rounding were off
+  // by 1.9e-6): S = lam^n S0 + sum_t (lam^{n-1-t} v_t) k_t^T.
+  const float gh = delta ? 0.f : floor_decay(p.g[h]);
   float *ks = stage, *vs = stage + n * DK;
 #pragma unroll 2
   for (int x = tid; x < n * (DK / 8); x += 128) {
@@ -529,6 +534,11 @@ tree_commit_kernel(const CommitParams p) {
     const int t = x / (DV / 8), d = 8 * (x - t * (DV / 8));
     float y[8];
     rows::load8(static_cast<const T *>(p.v) + (((size_t)b * M + path[n - 1 - t]) * p.Hv + h) * DV + d, y);
+    if (!delta) {
+      const float w = expf(gh * (float)(n - 1 - t));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] *= w;
+    }
 #pragma unroll
     for (int e = 0; e < 8; e += 4)
       *reinterpret_cast<float4 *>(vs + t * DV + d + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
@@ -539,8 +549,7 @@ tree_commit_kernel(const CommitParams p) {
       al[t] = p.raw ? alpha_raw(p.g[gi]) : expf(p.g[gi]);
       bt[t] = p.raw ? beta_raw(p.beta[gi]) : p.beta[gi];
     } else {
-      al[t] = expf(floor_decay(p.g[h]));
-      bt[t] = 1.f;
+      al[t] = t == 0 ? expf(gh * (float)n) : 1.f;
     }
   }
   __syncthreads();
